@@ -246,6 +246,71 @@ moe_status_t moe_fwd_noalloc(const moe_desc_t* desc, const void* hidden,
                              size_t saved_bytes, int32_t* bad_ids,
                              hipStream_t stream);
 
+/* Forward for a few tokens (decoding): T <= MOE_FEW_MAX_TOKENS, else
+ * MOE_ERR_UNSUPPORTED.  Computes moe_fwd's out without its routing pass and
+ * without `saved` (no backward): each active expert's weights are read once,
+ * by kernels sized for one or two slots an expert.  a = phi(..) is rounded to
+ * the activations' type as in moe_fwd; sums over H, I and K are fp32 in a fixed
+ * order (not moe_fwd's order, so the two agree to rounding, not bit for bit).
+ * MOE_ERR_UNSUPPORTED also where 64 rows of the weights, hidden, or a [S,I]
+ * reach 2^31 bytes.  ws: at least moe_few_workspace_size() bytes (its first
+ * word is the status that moe_check_device_status reports); nothing in it has
+ * to start at zero.  Bad expert ids, T = 0, streams and errors as for
+ * moe_fwd.  moe_fwd_few_logits takes router logits [T,E] and writes the ids
+ * and weights it chose, as moe_fwd_logits does. */
+#define MOE_FEW_MAX_TOKENS 128
+moe_status_t moe_few_workspace_size(const moe_desc_t* desc, size_t* ws_bytes);
+moe_status_t moe_fwd_few(const moe_desc_t* desc, const void* hidden,
+                         const int32_t* topk_ids, const float* topk_weights,
+                         const void* w_gate_up, const void* w_down, void* out,
+                         void* ws, size_t ws_bytes, hipStream_t stream);
+moe_status_t moe_fwd_few_logits(const moe_desc_t* desc, const void* hidden,
+                                const float* logits, const void* w_gate_up,
+                                const void* w_down, void* out,
+                                int32_t* topk_ids, float* topk_weights,
+                                void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Weight rows in 4-bit microscaled floating point (the OCP MXFP4 element and
+ * scale formats): blocks of 32 consecutive columns share one E8M0 scale byte
+ * s, each element is an E2M1 code c (sign, 2 exponent bits, 1 mantissa bit:
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) and stands for
+ * c * 2^(s - 127); s = 255 makes its block NaN.
+ *   codes  uint8 [rows, cols/2]: column 2i in the low, 2i+1 in the high half
+ *   scales uint8 [rows, cols/32]
+ * moe_mx_quantize: s - 127 = max(floor(log2(max |w|)) - 2, -127) over the
+ * block, the code is the nearest to w / 2^(s-127), ties to the even code,
+ * magnitudes beyond 6 become 6; a block with an infinity or NaN gets s = 255
+ * and zero codes.  moe_mx_dequantize gives the values the codes stand for
+ * (exact in bf16 and fp32).  w: [rows, cols] of `dtype` (moe_dtype_t); cols a
+ * multiple of 32, else MOE_ERR_UNSUPPORTED; rows = 0 does nothing. */
+moe_status_t moe_mx_quantize(const void* w, int32_t dtype, int64_t rows,
+                             int64_t cols, void* codes, void* scales,
+                             hipStream_t stream);
+moe_status_t moe_mx_dequantize(const void* codes, const void* scales,
+                               int32_t dtype, int64_t rows, int64_t cols,
+                               void* w, hipStream_t stream);
+
+/* Forward on expert weights in that form: gu_codes [E,2I,H/2], gu_scales
+ * [E,2I,H/32] in the descriptor's gate/up layout, d_codes [E,H,I/2], d_scales
+ * [E,H,I/32]; hidden, out and a = phi(..) are bf16 and products accumulate in
+ * fp32.  Computes what moe_fwd computes on the weights moe_mx_dequantize
+ * gives.  dtype must be MOE_BF16 and H and I multiples of 32, else
+ * MOE_ERR_UNSUPPORTED.  ws: at least moe_mx_workspace_size() bytes.
+ * Everything else as for moe_fwd (no `saved`, no backward);
+ * moe_mx_fwd_logits is to it as moe_fwd_logits to moe_fwd. */
+moe_status_t moe_mx_workspace_size(const moe_desc_t* desc, size_t* ws_bytes);
+moe_status_t moe_mx_fwd(const moe_desc_t* desc, const void* hidden,
+                        const int32_t* topk_ids, const float* topk_weights,
+                        const void* gu_codes, const void* gu_scales,
+                        const void* d_codes, const void* d_scales, void* out,
+                        void* ws, size_t ws_bytes, hipStream_t stream);
+moe_status_t moe_mx_fwd_logits(const moe_desc_t* desc, const void* hidden,
+                               const float* logits, const void* gu_codes,
+                               const void* gu_scales, const void* d_codes,
+                               const void* d_scales, void* out,
+                               int32_t* topk_ids, float* topk_weights,
+                               void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* Synchronises `stream` and reports MOE_ERR_BAD_EXPERT_ID if the last
  * routing done in `ws` met an id outside [0,E), else MOE_OK. */
 moe_status_t moe_check_device_status(const void* ws, hipStream_t stream);

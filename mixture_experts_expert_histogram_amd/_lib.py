@@ -20,7 +20,12 @@ MOE_GU_CONCAT, MOE_GU_INTERLEAVED = 0, 1
 
 EXPORTED = ["moe_workspace_size", "moe_route_workspace_size", "moe_route", "moe_router", "moe_fwd",
             "moe_fwd_logits", "moe_fwd_sep", "moe_bwd", "moe_bwd_sep", "moe_router_bwd", "moe_check_device_status",
-            "moe_status_str", "moe_timing_enable", "moe_timing_disable", "moe_timing_read", "moe_fwd_noalloc"]
+            "moe_status_str", "moe_timing_enable", "moe_timing_disable", "moe_timing_read", "moe_fwd_noalloc",
+            "moe_few_workspace_size", "moe_fwd_few", "moe_fwd_few_logits", "moe_mx_quantize", "moe_mx_dequantize",
+            "moe_mx_workspace_size", "moe_mx_fwd", "moe_mx_fwd_logits"]
+
+# Most tokens of fwd_few (moe.h).
+FEW_MAX_TOKENS = 128
 
 # Size of the library's per-GPU scratch array behind moe_fwd_noalloc (moe.h).
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -70,6 +75,15 @@ def library() -> ctypes.CDLL:
     lib.moe_bwd_sep.argtypes = [pd, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_bwd.argtypes = [pd, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_fwd_noalloc.argtypes = [pd, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
+    lib.moe_few_workspace_size.argtypes = [pd, psz]
+    lib.moe_fwd_few.argtypes = [pd, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_fwd_few_logits.argtypes = [pd, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_mx_quantize.argtypes = [vp, i32, i64, i64, vp, vp, vp]
+    lib.moe_mx_dequantize.argtypes = [vp, vp, i32, i64, i64, vp, vp]
+    lib.moe_mx_workspace_size.argtypes = [pd, psz]
+    lib.moe_mx_fwd.argtypes = [pd, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_mx_fwd_logits.argtypes = [pd, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_check_device_status.argtypes = [vp, vp]
     lib.moe_status_str.argtypes = [ctypes.c_int]
     lib.moe_status_str.restype = ctypes.c_char_p
@@ -79,7 +93,8 @@ def library() -> ctypes.CDLL:
     for name in ["moe_workspace_size", "moe_route_workspace_size", "moe_route", "moe_router", "moe_fwd",
                  "moe_fwd_logits", "moe_fwd_sep", "moe_bwd", "moe_bwd_sep", "moe_router_bwd",
                  "moe_check_device_status", "moe_timing_enable", "moe_timing_disable", "moe_timing_read",
-                 "moe_fwd_noalloc"]:
+                 "moe_fwd_noalloc", "moe_few_workspace_size", "moe_fwd_few", "moe_fwd_few_logits", "moe_mx_quantize",
+                 "moe_mx_dequantize", "moe_mx_workspace_size", "moe_mx_fwd", "moe_mx_fwd_logits"]:
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -362,6 +377,186 @@ def bwd_sep(hidden, topk_ids, topk_weights, w_gate, w_up, w_down, d_out, saved=N
                                  _ptr(dw), _ptr(dg), _ptr(du), _ptr(dd), _ptr(ws), ws.numel(), _stream()),
            "moe_bwd_sep")
     return dh, dw, dg, du, dd, ws
+
+
+# ---------------------------------------------------------------- few tokens, 4-bit weights
+def _launch(device, where: str, f, *args):
+    """Call f(*args, stream) on the current stream of the tensors' device."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        _check(f(*args, _stream()), where)
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args, _stream()), where)
+
+
+def _need(t, name: str, shape, dtype, device):
+    """t must be a contiguous tensor of this shape and type on the device."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _size_of(f, desc: MoeDesc, where: str) -> int:
+    n = ctypes.c_size_t()
+    _check(f(ctypes.byref(desc), ctypes.byref(n)), where)
+    return n.value
+
+
+def few_workspace_size(desc: MoeDesc) -> int:
+    return _size_of(library().moe_few_workspace_size, desc, "moe_few_workspace_size")
+
+
+def mx_workspace_size(desc: MoeDesc) -> int:
+    return _size_of(library().moe_mx_workspace_size, desc, "moe_mx_workspace_size")
+
+
+def _served(where, size_of, hidden, routing, K, weights, E, I, act, layout, limit, alpha, ws, out):
+    """Shared call of the serving forwards.  routing: (topk_ids, topk_weights), or the logits [T,E] when K is given."""
+    import torch
+    if not hidden.is_cuda or hidden.dim() != 2:
+        raise ValueError("hidden must be a device tensor [T, H]")
+    dev = hidden.device
+    T, H = hidden.shape
+    dt = "bf16" if hidden.dtype == torch.bfloat16 else ("fp32" if hidden.dtype == torch.float32 else None)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {hidden.dtype}")
+    _need(hidden, "hidden", (T, H), hidden.dtype, dev)
+    logits = None
+    if K is not None:
+        logits = _f32(routing)
+        _need(logits, "logits", (T, E), torch.float32, dev)
+        ids = torch.empty((T, int(K)), dtype=torch.int32, device=dev)
+        w = torch.empty((T, int(K)), dtype=torch.float32, device=dev)
+    else:
+        ids, w = _ids32(routing[0]), _f32(routing[1])
+        if ids.dim() != 2:
+            raise ValueError("topk_ids must be [T, K]")
+        _need(ids, "topk_ids", (T, ids.shape[1]), torch.int32, dev)
+        _need(w, "topk_weights", ids.shape, torch.float32, dev)
+    d = make_desc(T, H, I, E, ids.shape[1], dt, act, layout, limit, alpha)
+    if ws is None:
+        ws = empty_workspace(size_of(d), dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous, on {dev}")
+    if out is None:
+        out = torch.empty_like(hidden)
+    else:
+        _need(out, "out", (T, H), hidden.dtype, dev)
+    f = getattr(library(), where)
+    wp = [t.data_ptr() for t in weights]
+    if logits is None:
+        _launch(dev, where, f, ctypes.byref(d), _ptr(hidden), _ptr(ids), _ptr(w), *wp, _ptr(out), _ptr(ws), _nbytes(ws))
+    else:
+        _launch(dev, where, f, ctypes.byref(d), _ptr(hidden), _ptr(logits), *wp, _ptr(out), _ptr(ids), _ptr(w), _ptr(ws),
+                _nbytes(ws))
+    return out, ids, w, ws
+
+
+def _dense_experts(hidden, w_gate_up, w_down):
+    """(E, I) of plain expert weights [E,2I,H], [E,H,I] of hidden's type."""
+    if w_gate_up.dim() != 3 or w_gate_up.shape[1] % 2:
+        raise ValueError("w_gate_up must be [E, 2I, H]")
+    E, I = w_gate_up.shape[0], w_gate_up.shape[1] // 2
+    H = hidden.shape[-1]
+    _need(w_gate_up, "w_gate_up", (E, 2 * I, H), hidden.dtype, hidden.device)
+    _need(w_down, "w_down", (E, H, I), hidden.dtype, hidden.device)
+    return E, I
+
+
+def fwd_few(hidden, topk_ids, topk_weights, w_gate_up, w_down, act="swiglu", layout="concat", limit=7.0, alpha=1.702,
+            ws=None, out=None):
+    """Forward for at most FEW_MAX_TOKENS tokens (decoding); returns (out, ws).  No backward."""
+    E, I = _dense_experts(hidden, w_gate_up, w_down)
+    out, _, _, ws = _served("moe_fwd_few", few_workspace_size, hidden, (topk_ids, topk_weights), None,
+                            (w_gate_up, w_down), E, I, act, layout, limit, alpha, ws, out)
+    return out, ws
+
+
+def fwd_few_logits(hidden, logits, K: int, w_gate_up, w_down, act="swiglu", layout="concat", limit=7.0, alpha=1.702,
+                   ws=None, out=None):
+    """fwd_few from router logits [T,E]; returns (out, topk_ids, topk_weights, ws)."""
+    E, I = _dense_experts(hidden, w_gate_up, w_down)
+    return _served("moe_fwd_few_logits", few_workspace_size, hidden, logits, K, (w_gate_up, w_down), E, I, act, layout,
+                   limit, alpha, ws, out)
+
+
+def mx_quantize(w, out=None):
+    """Rows of w [..., C] (bf16 or fp32, C a multiple of 32) in 4-bit microscaled floating point; returns
+    (codes uint8 [..., C/2], scales uint8 [..., C/32])."""
+    import torch
+    if not w.is_cuda or w.dim() < 1 or not w.is_contiguous():
+        raise ValueError("mx_quantize takes a contiguous device tensor [..., C]")
+    if w.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"unsupported dtype {w.dtype}")
+    C = w.shape[-1]
+    if C < 1 or C % 32:
+        raise ValueError(f"the last dimension must be a multiple of 32, got {C}")
+    lead = tuple(w.shape[:-1])
+    if out is None:
+        out = (torch.empty(lead + (C // 2,), dtype=torch.uint8, device=w.device),
+               torch.empty(lead + (C // 32,), dtype=torch.uint8, device=w.device))
+    codes, scales = out
+    _need(codes, "codes", lead + (C // 2,), torch.uint8, w.device)
+    _need(scales, "scales", lead + (C // 32,), torch.uint8, w.device)
+    _launch(w.device, "moe_mx_quantize", library().moe_mx_quantize, _ptr(w),
+            MOE_BF16 if w.dtype == torch.bfloat16 else MOE_F32, w.numel() // C, C, _ptr(codes), _ptr(scales))
+    return codes, scales
+
+
+def mx_dequantize(codes, scales, dtype="bf16", out=None):
+    """The values that codes [..., C/2] and scales [..., C/32] stand for, as bf16 or fp32 [..., C] (exact)."""
+    import torch
+    if not codes.is_cuda or codes.dim() < 1:
+        raise ValueError("mx_dequantize takes device tensors")
+    lead, C = tuple(codes.shape[:-1]), 2 * codes.shape[-1]
+    if C < 1 or C % 32:
+        raise ValueError(f"codes must hold whole blocks of 32 columns, got {C} columns")
+    _need(codes, "codes", lead + (C // 2,), torch.uint8, codes.device)
+    _need(scales, "scales", lead + (C // 32,), torch.uint8, codes.device)
+    kind = _dt(dtype)
+    tdt = torch.bfloat16 if kind == MOE_BF16 else torch.float32
+    if out is None:
+        out = torch.empty(lead + (C,), dtype=tdt, device=codes.device)
+    _need(out, "out", lead + (C,), tdt, codes.device)
+    _launch(codes.device, "moe_mx_dequantize", library().moe_mx_dequantize, _ptr(codes), _ptr(scales), kind,
+            out.numel() // C, C, _ptr(out))
+    return out
+
+
+def _mx_experts(hidden, gate_up, down):
+    """(E, I) of expert weights as (codes, scales) pairs."""
+    import torch
+    (gc, gs), (dc, ds) = gate_up, down
+    if gc.dim() != 3 or gc.shape[1] % 2:
+        raise ValueError("gate_up codes must be [E, 2I, H/2]")
+    E, I = gc.shape[0], gc.shape[1] // 2
+    H, dev = hidden.shape[-1], hidden.device
+    if hidden.dtype != torch.bfloat16 or H % 32 or I % 32:
+        raise ValueError("4-bit experts take bf16 hidden states, H and I multiples of 32")
+    _need(gc, "gate_up codes", (E, 2 * I, H // 2), torch.uint8, dev)
+    _need(gs, "gate_up scales", (E, 2 * I, H // 32), torch.uint8, dev)
+    _need(dc, "down codes", (E, H, I // 2), torch.uint8, dev)
+    _need(ds, "down scales", (E, H, I // 32), torch.uint8, dev)
+    return E, I
+
+
+def mx_fwd(hidden, topk_ids, topk_weights, gate_up, down, act="swiglu", layout="concat", limit=7.0, alpha=1.702, ws=None,
+           out=None):
+    """Forward on 4-bit expert weights: gate_up and down are the (codes, scales) of mx_quantize(w_gate_up [E,2I,H])
+    and mx_quantize(w_down [E,H,I]); hidden is bf16.  Returns (out, ws).  No backward."""
+    E, I = _mx_experts(hidden, gate_up, down)
+    out, _, _, ws = _served("moe_mx_fwd", mx_workspace_size, hidden, (topk_ids, topk_weights), None,
+                            (*gate_up, *down), E, I, act, layout, limit, alpha, ws, out)
+    return out, ws
+
+
+def mx_fwd_logits(hidden, logits, K: int, gate_up, down, act="swiglu", layout="concat", limit=7.0, alpha=1.702, ws=None,
+                  out=None):
+    """mx_fwd from router logits [T,E]; returns (out, topk_ids, topk_weights, ws)."""
+    E, I = _mx_experts(hidden, gate_up, down)
+    return _served("moe_mx_fwd_logits", mx_workspace_size, hidden, logits, K, (*gate_up, *down), E, I, act, layout, limit,
+                   alpha, ws, out)
 
 
 def check_device_status(ws) -> int:

@@ -1,6 +1,7 @@
 // C ABI of the routed MoE expert computation: argument checks, workspace
 // layout and the launch sequence of the forward and backward passes.
 #include "../../include/moe.h"
+#include "few.h"
 #include "moe_internal.h"
 
 #include <string.h>
@@ -429,6 +430,198 @@ moe_status_t moe_bwd_sep(const moe_desc_t* desc, const void* hidden, const int32
   if (!w_up || !d_w_up) return MOE_ERR_INVALID_ARG;
   return bwd_impl(desc, hidden, topk_ids, topk_weights, w_gate, w_up, w_down, d_out, saved, saved_bytes, d_hidden,
                   d_topk_weights, d_w_gate, d_w_up, d_w_down, ws, ws_bytes, stream);
+}
+
+// ------------------------------------------------------------ few tokens, 4-bit weights
+}  // extern "C"
+
+namespace {
+
+// Workspace of the few-token path: status word, a, per-slot down outputs.
+struct FewLayout {
+  size_t a, y, end;
+};
+FewLayout few_layout(const Dims& d) {
+  FewLayout L;
+  L.a = align_up(4 * sizeof(int32_t));
+  L.y = L.a + align_up((size_t)d.S * d.I * d.esz);
+  L.end = L.y + align_up((size_t)d.S * d.H * sizeof(float));
+  return L;
+}
+
+// The kernels' limits: 32-bit byte offsets from a tile's first weight row,
+// from hidden and from a.
+moe_status_t few_check(const Dims& d) {
+  const int64_t lim = int64_t(1) << 31;
+  if (d.T > FEW_MAX_T) return MOE_ERR_UNSUPPORTED;
+  if (64 * d.H * (int64_t)d.esz >= lim || 64 * d.I * (int64_t)d.esz >= lim) return MOE_ERR_UNSUPPORTED;
+  if (d.T * d.H * (int64_t)d.esz >= lim || d.S * d.I * (int64_t)d.esz >= lim) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// Microscaled 4-bit weights: whole blocks of 32 columns, bf16 activations.
+moe_status_t mx_check(const Dims& d) {
+  if (d.esz != 2 || d.H % 32 != 0 || d.I % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+struct LayerPtrs {
+  const void* hidden;
+  const float* logits;    // or null: ids and weights are inputs
+  int32_t* ids;
+  float* w;
+  const void *gu, *gus, *dn, *dns;   // weights, and their scales (null: plain weights)
+  void* out;
+};
+
+// Pointer checks shared by the few-token and 4-bit forwards.
+moe_status_t check_ptrs(const Dims& d, const LayerPtrs& p, bool mx, const void* ws) {
+  if (!p.gu || !p.dn || !ws || (mx && (!p.gus || !p.dns))) return MOE_ERR_INVALID_ARG;
+  if (d.T > 0 && (!p.hidden || !p.ids || !p.w || !p.out)) return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {p.hidden, p.logits, p.ids, p.w, p.gu, p.gus, p.dn, p.dns, p.out, ws};
+  for (const void* q : ptrs)
+    if (q && !aligned16(q)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status_t run_few(const moe_desc_t* desc, const Dims& d, const LayerPtrs& p, bool mx, void* ws,
+                     hipStream_t stream) {
+  const FewLayout L = few_layout(d);
+  char* b = (char*)ws;
+  if (p.logits) HIP_TRY(launch_topk(p.logits, (int)d.T, (int)d.K, (int)d.E, p.ids, p.w, stream));
+  FewArgs a = {};
+  a.ids = p.ids; a.w = p.w; a.X = p.hidden;
+  const bool inter = desc->gu_layout == MOE_GU_INTERLEAVED;
+  const long row = mx ? d.H / 2 : d.H * (long)d.esz;   // bytes of a gate or up row
+  a.gu_es = 2 * d.I * row;
+  a.gu_rs = inter ? 2 * row : row;
+  const long up = inter ? row : d.I * row;
+  a.gu_g = p.gu; a.gu_u = (const char*)p.gu + up;
+  a.Wd = p.dn;
+  a.d_rs = mx ? d.I / 2 : d.I * (long)d.esz;
+  if (mx) {
+    a.gus_g = p.gus; a.gus_u = (const char*)p.gus + up / 16;
+    a.sd = p.dns;
+  }
+  a.a = b + L.a; a.y = (float*)(b + L.y); a.out = p.out; a.status = (int32_t*)b;
+  a.T = (int)d.T; a.H = (int)d.H; a.I = (int)d.I; a.E = (int)d.E; a.K = (int)d.K; a.S = (int)d.S;
+  a.act = desc->act == MOE_CLAMPED_GLU; a.limit = desc->clamp_limit; a.alpha = desc->glu_alpha;
+  HIP_TRY(launch_few(mx ? 2 : desc->dtype == MOE_BF16 ? 0 : 1, a, stream));
+  return MOE_OK;
+}
+
+moe_status_t few_impl(const moe_desc_t* desc, const LayerPtrs& p, void* ws, size_t ws_bytes, hipStream_t stream) {
+  Dims d;
+  moe_status_t st = check_desc(desc, &d);
+  if (st != MOE_OK) return st;
+  if ((st = check_ptrs(d, p, false, ws)) != MOE_OK) return st;
+  if ((st = few_check(d)) != MOE_OK) return st;
+  if (ws_bytes < few_layout(d).end) return MOE_ERR_WORKSPACE;
+  if (d.T == 0) {
+    HIP_TRY(launch_fill_zero(ws, 4 * sizeof(int32_t), stream));
+    return MOE_OK;
+  }
+  return run_few(desc, d, p, false, ws, stream);
+}
+
+moe_status_t mx_impl(const moe_desc_t* desc, const LayerPtrs& p, void* ws, size_t ws_bytes, hipStream_t stream) {
+  Dims d;
+  moe_status_t st = check_desc(desc, &d);
+  if (st != MOE_OK) return st;
+  if ((st = mx_check(d)) != MOE_OK) return st;
+  if ((st = check_ptrs(d, p, true, ws)) != MOE_OK) return st;
+  if ((st = few_check(d)) != MOE_OK) return st;
+  if (ws_bytes < few_layout(d).end) return MOE_ERR_WORKSPACE;
+  if (d.T == 0) {
+    HIP_TRY(launch_fill_zero(ws, 4 * sizeof(int32_t), stream));
+    return MOE_OK;
+  }
+  return run_few(desc, d, p, true, ws, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_few_workspace_size(const moe_desc_t* desc, size_t* ws_bytes) {
+  Dims d;
+  moe_status_t st = check_desc(desc, &d);
+  if (st != MOE_OK) return st;
+  if (!ws_bytes) return MOE_ERR_INVALID_ARG;
+  if ((st = few_check(d)) != MOE_OK) return st;
+  *ws_bytes = few_layout(d).end;
+  return MOE_OK;
+}
+
+moe_status_t moe_fwd_few(const moe_desc_t* desc, const void* hidden, const int32_t* topk_ids,
+                         const float* topk_weights, const void* w_gate_up, const void* w_down, void* out, void* ws,
+                         size_t ws_bytes, hipStream_t stream) {
+  const LayerPtrs p = {hidden, nullptr, (int32_t*)topk_ids, (float*)topk_weights, w_gate_up, nullptr, w_down, nullptr,
+                       out};
+  return few_impl(desc, p, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_fwd_few_logits(const moe_desc_t* desc, const void* hidden, const float* logits,
+                                const void* w_gate_up, const void* w_down, void* out, int32_t* topk_ids,
+                                float* topk_weights, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (desc && desc->T > 0 && !logits) return MOE_ERR_INVALID_ARG;
+  if (desc && desc->K > desc->E) return MOE_ERR_INVALID_ARG;
+  const LayerPtrs p = {hidden, logits, topk_ids, topk_weights, w_gate_up, nullptr, w_down, nullptr, out};
+  return few_impl(desc, p, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_mx_workspace_size(const moe_desc_t* desc, size_t* ws_bytes) {
+  Dims d;
+  moe_status_t st = check_desc(desc, &d);
+  if (st != MOE_OK) return st;
+  if (!ws_bytes) return MOE_ERR_INVALID_ARG;
+  if ((st = mx_check(d)) != MOE_OK) return st;
+  if ((st = few_check(d)) != MOE_OK) return st;
+  *ws_bytes = few_layout(d).end;
+  return MOE_OK;
+}
+
+moe_status_t moe_mx_fwd(const moe_desc_t* desc, const void* hidden, const int32_t* topk_ids,
+                        const float* topk_weights, const void* gu_codes, const void* gu_scales, const void* d_codes,
+                        const void* d_scales, void* out, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const LayerPtrs p = {hidden, nullptr, (int32_t*)topk_ids, (float*)topk_weights, gu_codes, gu_scales, d_codes,
+                       d_scales, out};
+  return mx_impl(desc, p, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_mx_fwd_logits(const moe_desc_t* desc, const void* hidden, const float* logits, const void* gu_codes,
+                               const void* gu_scales, const void* d_codes, const void* d_scales, void* out,
+                               int32_t* topk_ids, float* topk_weights, void* ws, size_t ws_bytes,
+                               hipStream_t stream) {
+  if (desc && desc->T > 0 && !logits) return MOE_ERR_INVALID_ARG;
+  if (desc && desc->K > desc->E) return MOE_ERR_INVALID_ARG;
+  const LayerPtrs p = {hidden, logits, topk_ids, topk_weights, gu_codes, gu_scales, d_codes, d_scales, out};
+  return mx_impl(desc, p, ws, ws_bytes, stream);
+}
+
+static moe_status_t mx_rows_check(int64_t rows, int64_t cols, int32_t dtype, const void* w, const void* codes,
+                                  const void* scales) {
+  if (rows < 0 || cols < 1 || (dtype != MOE_BF16 && dtype != MOE_F32)) return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && (!w || !codes || !scales)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+  if (cols % 32 != 0 || cols >= (int64_t(1) << 31) || rows > (int64_t(1) << 42) / cols) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t moe_mx_quantize(const void* w, int32_t dtype, int64_t rows, int64_t cols, void* codes, void* scales,
+                             hipStream_t stream) {
+  const moe_status_t st = mx_rows_check(rows, cols, dtype, w, codes, scales);
+  if (st != MOE_OK) return st;
+  HIP_TRY(launch_mx_quantize(dtype == MOE_BF16 ? 0 : 1, w, (long)(rows * cols), codes, scales, stream));
+  return MOE_OK;
+}
+
+moe_status_t moe_mx_dequantize(const void* codes, const void* scales, int32_t dtype, int64_t rows, int64_t cols,
+                               void* w, hipStream_t stream) {
+  const moe_status_t st = mx_rows_check(rows, cols, dtype, w, codes, scales);
+  if (st != MOE_OK) return st;
+  HIP_TRY(launch_mx_dequantize(dtype == MOE_BF16 ? 0 : 1, codes, scales, (long)(rows * cols), w, stream));
+  return MOE_OK;
 }
 
 // ------------------------------------------------------------ no-allocation forward

@@ -66,7 +66,9 @@ inline hipError_t run_kernel(const char* name, hipStream_t stream, F&& launch) {
 // ---- routing / combine / reduce (route.hip)
 hipError_t launch_route(const int32_t* ids, const float* w, int S, int K, int E,
                         const RouteState& rs, hipStream_t stream);
-// router: top-K of logits [T,E] and their softmax -> ids, w [T,K]; then as launch_route
+// router: top-K of logits [T,E] and their softmax -> ids, w [T,K]
+hipError_t launch_topk(const float* logits, int T, int K, int E, int32_t* ids, float* w, hipStream_t stream);
+// launch_topk, then as launch_route
 hipError_t launch_route_logits(const float* logits, int T, int K, int E, int32_t* ids, float* w,
                                const RouteState& rs, hipStream_t stream);
 // d_logits [T,E] from the routing-weight gradient through the softmax over the chosen K
@@ -79,6 +81,11 @@ hipError_t launch_topkw_reduce(const float* partials, int nparts, const int32_t*
                                float* dw, hipStream_t stream);
 hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t stream);
 hipError_t launch_copy_i32(const int32_t* src, int32_t* dst, int n, hipStream_t stream);
+
+// ---- microscaled 4-bit rows (mx.hip); n elements, dtype 0 bf16, 1 fp32
+hipError_t launch_mx_quantize(int dtype, const void* w, long n, void* codes, void* scales, hipStream_t stream);
+hipError_t launch_mx_dequantize(int dtype, const void* codes, const void* scales, long n, void* w,
+                                hipStream_t stream);
 
 // ---- grouped GEMMs (gemm.hip)
 struct GemmProblem {

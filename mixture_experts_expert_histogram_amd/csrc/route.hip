@@ -349,11 +349,15 @@ hipError_t launch_route(const int32_t* ids, const float* w, int S, int K, int E,
   });
 }
 
-hipError_t launch_route_logits(const float* logits, int T, int K, int E, int32_t* ids, float* w,
-                               const RouteState& rs, hipStream_t stream) {
-  hipError_t err = run_kernel("route_logits", stream, [&] {
+hipError_t launch_topk(const float* logits, int T, int K, int E, int32_t* ids, float* w, hipStream_t stream) {
+  return run_kernel("route_logits", stream, [&] {
     route_logits_kernel<<<(T + 3) / 4, 256, 0, stream>>>(logits, T, E, K, ids, w);
   });
+}
+
+hipError_t launch_route_logits(const float* logits, int T, int K, int E, int32_t* ids, float* w,
+                               const RouteState& rs, hipStream_t stream) {
+  const hipError_t err = launch_topk(logits, T, K, E, ids, w, stream);
   if (err != hipSuccess) return err;
   return launch_route(ids, w, T * K, K, E, rs, stream);
 }
