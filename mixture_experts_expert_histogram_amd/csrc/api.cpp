@@ -2,6 +2,7 @@
 // layout and the launch sequence of the forward and backward passes.
 #include "../../include/moe.h"
 #include "few.h"
+#include "gemm_mx.h"
 #include "moe_internal.h"
 
 #include <string.h>
@@ -461,9 +462,18 @@ moe_status_t few_check(const Dims& d) {
 
 // Microscaled 4-bit weights: whole blocks of 32 columns, bf16 activations.
 moe_status_t mx_check(const Dims& d) {
+  const int64_t lim = int64_t(1) << 31;
   if (d.esz != 2 || d.H % 32 != 0 || d.I % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  // 32-bit byte offsets from hidden, from a tile's rows of a (128) and from its weight rows; the grid
+  if (d.H >= (1 << 23) || d.I >= (1 << 23) || d.T * d.H * 2 >= lim) return MOE_ERR_UNSUPPORTED;
+  const int64_t wide = d.H > d.I ? d.H : d.I;
+  if ((d.S / 128 + d.E + 1) * (wide / 128 + 1) >= lim / 2) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
+
+// Whether the 4-bit layer runs on the few-token kernels.
+bool mx_few(const Dims& d) { return few_check(d) == MOE_OK; }
+size_t mx_ws(const Dims& d) { return mx_few(d) ? few_layout(d).end : make_layout(d).f_end; }
 
 struct LayerPtrs {
   const void* hidden;
@@ -530,13 +540,34 @@ moe_status_t mx_impl(const moe_desc_t* desc, const LayerPtrs& p, void* ws, size_
   if (st != MOE_OK) return st;
   if ((st = mx_check(d)) != MOE_OK) return st;
   if ((st = check_ptrs(d, p, true, ws)) != MOE_OK) return st;
-  if ((st = few_check(d)) != MOE_OK) return st;
-  if (ws_bytes < few_layout(d).end) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < mx_ws(d)) return MOE_ERR_WORKSPACE;
   if (d.T == 0) {
     HIP_TRY(launch_fill_zero(ws, 4 * sizeof(int32_t), stream));
     return MOE_OK;
   }
-  return run_few(desc, d, p, true, ws, stream);
+  if (mx_few(d)) return run_few(desc, d, p, true, ws, stream);
+  const Layout L = make_layout(d);
+  RouteState rs = route_state(ws, L, d);
+  const GemmProblem pb = problem(desc, d, &rs);
+  char* b = (char*)ws;
+  float* yp = (float*)(b + L.f_y);
+  if (p.logits)
+    HIP_TRY(launch_route_logits(p.logits, (int)d.T, (int)d.K, (int)d.E, p.ids, p.w, rs, stream));
+  else
+    HIP_TRY(launch_route(p.ids, p.w, (int)d.S, (int)d.K, (int)d.E, rs, stream));
+  const bool inter = desc->gu_layout == MOE_GU_INTERLEAVED;
+  MxWeights w = {};
+  const long row = d.H / 2;
+  w.gu_es = 2 * d.I * row;
+  w.gu_rs = inter ? 2 * row : row;
+  const long up = inter ? row : d.I * row;
+  w.gu_g = p.gu; w.gu_u = (const char*)p.gu + up;
+  w.gus_g = p.gus; w.gus_u = (const char*)p.gus + up / 16;
+  w.Wd = p.dn; w.sd = p.dns;
+  HIP_TRY(launch_mx_gate_up(pb, w, p.hidden, b + L.f_a, stream));
+  HIP_TRY(launch_mx_down(pb, w, b + L.f_a, yp, stream));
+  HIP_TRY(launch_combine(pb.dtype, yp, rs.inv_pos, (int)d.T, (int)d.K, (int)d.H, p.out, stream));
+  return MOE_OK;
 }
 
 }  // namespace
@@ -576,8 +607,7 @@ moe_status_t moe_mx_workspace_size(const moe_desc_t* desc, size_t* ws_bytes) {
   if (st != MOE_OK) return st;
   if (!ws_bytes) return MOE_ERR_INVALID_ARG;
   if ((st = mx_check(d)) != MOE_OK) return st;
-  if ((st = few_check(d)) != MOE_OK) return st;
-  *ws_bytes = few_layout(d).end;
+  *ws_bytes = mx_ws(d);
   return MOE_OK;
 }
 
