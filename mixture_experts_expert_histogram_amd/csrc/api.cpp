@@ -472,7 +472,8 @@ moe_status_t mx_check(const Dims& d) {
 }
 
 // Whether the 4-bit layer runs on the few-token kernels.
-bool mx_few(const Dims& d) { return few_check(d) == MOE_OK; }
+// Those hold a workgroup's scales in LDS: rows of at most 8192.
+bool mx_few(const Dims& d) { return few_check(d) == MOE_OK && d.H <= 8192 && d.I <= 8192; }
 size_t mx_ws(const Dims& d) { return mx_few(d) ? few_layout(d).end : make_layout(d).f_end; }
 
 struct LayerPtrs {
@@ -498,8 +499,8 @@ moe_status_t run_few(const moe_desc_t* desc, const Dims& d, const LayerPtrs& p, 
                      hipStream_t stream) {
   const FewLayout L = few_layout(d);
   char* b = (char*)ws;
-  if (p.logits) HIP_TRY(launch_topk(p.logits, (int)d.T, (int)d.K, (int)d.E, p.ids, p.w, stream));
   FewArgs a = {};
+  a.logits = p.logits; a.ids_out = p.ids; a.w_out = p.w;
   a.ids = p.ids; a.w = p.w; a.X = p.hidden;
   const bool inter = desc->gu_layout == MOE_GU_INTERLEAVED;
   const long row = mx ? d.H / 2 : d.H * (long)d.esz;   // bytes of a gate or up row

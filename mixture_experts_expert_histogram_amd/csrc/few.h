@@ -12,8 +12,11 @@ constexpr int FEW_MAX_T = 128;
 // after gu_g (gu_u); mx scales follow the same strides over 16 (a row of c
 // code bytes has c / 16 scales).  Rows of Wd are d_rs bytes, H an expert.
 struct FewArgs {
+  const float* logits;  // [T,E], or null: ids and w are given
   const int32_t* ids;   // [T,K]
   const float* w;       // [T,K]
+  int32_t* ids_out;     // with logits: where the choice goes (ids, w)
+  float* w_out;
   const void* X;        // [T,H]
   const void* gu_g;
   const void* gu_u;
