@@ -380,19 +380,30 @@ def bwd_sep(hidden, topk_ids, topk_weights, w_gate, w_up, w_down, d_out, saved=N
 
 
 # ---------------------------------------------------------------- few tokens, 4-bit weights
+# A decode step's calls take a few microseconds on the GPU, so their host side is kept short: the binding's functions are
+# looked up once, sizes of a descriptor are kept, and checks run on what the caller passed only.
+def _raw_stream(index: int) -> int:
+    """The current stream of a device as an integer, by torch's direct query where it has one (0.1 us against 3)."""
+    import torch
+    q = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return q(index) if q is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _launch(device, where: str, f, *args):
     """Call f(*args, stream) on the current stream of the tensors' device."""
     import torch
     if device.index == torch.cuda.current_device():
-        _check(f(*args, _stream()), where)
+        status = f(*args, _raw_stream(device.index))
     else:
         with torch.cuda.device(device):
-            _check(f(*args, _stream()), where)
+            status = f(*args, _raw_stream(device.index))
+    if status != MOE_OK:
+        raise MoeError(status, where)
 
 
 def _need(t, name: str, shape, dtype, device):
     """t must be a contiguous tensor of this shape and type on the device."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
@@ -411,11 +422,27 @@ def mx_workspace_size(desc: MoeDesc) -> int:
     return _size_of(library().moe_mx_workspace_size, desc, "moe_mx_workspace_size")
 
 
+_served_sizes = {}
+
+
+def _served_desc(size_of, *key):
+    """(descriptor, workspace bytes) of a serving call, kept by the descriptor's values (at most 4096 of them)."""
+    got = _served_sizes.get((size_of, key))
+    if got is None:
+        d = make_desc(*key)
+        if len(_served_sizes) >= 4096:
+            _served_sizes.clear()
+        got = _served_sizes[(size_of, key)] = (ctypes.byref(d), size_of(d))
+    return got
+
+
 def _served(where, size_of, hidden, routing, K, weights, E, I, act, layout, limit, alpha, ws, out):
     """Shared call of the serving forwards.  routing: (topk_ids, topk_weights), or the logits [T,E] when K is given."""
     import torch
     if not hidden.is_cuda or hidden.dim() != 2:
         raise ValueError("hidden must be a device tensor [T, H]")
+    if act not in ("swiglu", "clamped") or layout not in ("concat", "interleaved"):
+        raise ValueError(f"unknown act {act!r} or layout {layout!r}")
     dev = hidden.device
     T, H = hidden.shape
     dt = "bf16" if hidden.dtype == torch.bfloat16 else ("fp32" if hidden.dtype == torch.float32 else None)
@@ -434,9 +461,9 @@ def _served(where, size_of, hidden, routing, K, weights, E, I, act, layout, limi
             raise ValueError("topk_ids must be [T, K]")
         _need(ids, "topk_ids", (T, ids.shape[1]), torch.int32, dev)
         _need(w, "topk_weights", ids.shape, torch.float32, dev)
-    d = make_desc(T, H, I, E, ids.shape[1], dt, act, layout, limit, alpha)
+    d, nbytes = _served_desc(size_of, T, H, I, E, ids.shape[1], dt, act, layout, float(limit), float(alpha))
     if ws is None:
-        ws = empty_workspace(size_of(d), dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     elif ws.device != dev or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous, on {dev}")
     if out is None:
@@ -446,10 +473,11 @@ def _served(where, size_of, hidden, routing, K, weights, E, I, act, layout, limi
     f = getattr(library(), where)
     wp = [t.data_ptr() for t in weights]
     if logits is None:
-        _launch(dev, where, f, ctypes.byref(d), _ptr(hidden), _ptr(ids), _ptr(w), *wp, _ptr(out), _ptr(ws), _nbytes(ws))
-    else:
-        _launch(dev, where, f, ctypes.byref(d), _ptr(hidden), _ptr(logits), *wp, _ptr(out), _ptr(ids), _ptr(w), _ptr(ws),
+        _launch(dev, where, f, d, hidden.data_ptr(), ids.data_ptr(), w.data_ptr(), *wp, out.data_ptr(), ws.data_ptr(),
                 _nbytes(ws))
+    else:
+        _launch(dev, where, f, d, hidden.data_ptr(), logits.data_ptr(), *wp, out.data_ptr(), ids.data_ptr(), w.data_ptr(),
+                ws.data_ptr(), _nbytes(ws))
     return out, ids, w, ws
 
 
@@ -496,9 +524,11 @@ def mx_quantize(w, out=None):
     if out is None:
         out = (torch.empty(lead + (C // 2,), dtype=torch.uint8, device=w.device),
                torch.empty(lead + (C // 32,), dtype=torch.uint8, device=w.device))
-    codes, scales = out
-    _need(codes, "codes", lead + (C // 2,), torch.uint8, w.device)
-    _need(scales, "scales", lead + (C // 32,), torch.uint8, w.device)
+        codes, scales = out
+    else:
+        codes, scales = out
+        _need(codes, "codes", lead + (C // 2,), torch.uint8, w.device)
+        _need(scales, "scales", lead + (C // 32,), torch.uint8, w.device)
     _launch(w.device, "moe_mx_quantize", library().moe_mx_quantize, _ptr(w),
             MOE_BF16 if w.dtype == torch.bfloat16 else MOE_F32, w.numel() // C, C, _ptr(codes), _ptr(scales))
     return codes, scales
@@ -518,7 +548,8 @@ def mx_dequantize(codes, scales, dtype="bf16", out=None):
     tdt = torch.bfloat16 if kind == MOE_BF16 else torch.float32
     if out is None:
         out = torch.empty(lead + (C,), dtype=tdt, device=codes.device)
-    _need(out, "out", lead + (C,), tdt, codes.device)
+    else:
+        _need(out, "out", lead + (C,), tdt, codes.device)
     _launch(codes.device, "moe_mx_dequantize", library().moe_mx_dequantize, _ptr(codes), _ptr(scales), kind,
             out.numel() // C, C, _ptr(out))
     return out
