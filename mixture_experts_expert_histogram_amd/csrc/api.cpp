@@ -464,10 +464,10 @@ moe_status_t few_check(const Dims& d) {
 moe_status_t mx_check(const Dims& d) {
   const int64_t lim = int64_t(1) << 31;
   if (d.esz != 2 || d.H % 32 != 0 || d.I % 32 != 0) return MOE_ERR_UNSUPPORTED;
-  // 32-bit byte offsets from hidden, from a tile's rows of a (128) and from its weight rows; the grid
-  if (d.H >= (1 << 23) || d.I >= (1 << 23) || d.T * d.H * 2 >= lim) return MOE_ERR_UNSUPPORTED;
+  // a tile's scales in LDS; 32-bit byte offsets from hidden; the grid
+  if (d.H > MX_MAX_K || d.I > MX_MAX_K || d.T * d.H * 2 >= lim) return MOE_ERR_UNSUPPORTED;
   const int64_t wide = d.H > d.I ? d.H : d.I;
-  if ((d.S / 128 + d.E + 1) * (wide / 128 + 1) >= lim / 2) return MOE_ERR_UNSUPPORTED;
+  if ((d.S / 32 + d.E + 1) * (wide / 128 + 1) >= lim / 2) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

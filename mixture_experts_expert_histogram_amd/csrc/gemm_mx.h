@@ -12,12 +12,18 @@ struct MxWeights {
   long gu_es, gu_rs;
 };
 
+// LDS of a CU: the tile's scales (256 rows of K / 32 bytes) and two stages of
+// activations have to fit.
+constexpr int MX_MAX_LDS = 160 * 1024;
+constexpr int MX_MAX_K = 16384;
+
 struct MxArgs {
   GArgs g;
   const void *gu_g, *gu_u, *gus_g, *gus_u, *Wd, *sd;
   long gu_es, gu_rs;
 };
 
+int mx_tile_rows(const GemmProblem& pb);
 hipError_t launch_mx_gate_up(const GemmProblem& pb, const MxWeights& w, const void* X, void* a, hipStream_t s);
 hipError_t launch_mx_down(const GemmProblem& pb, const MxWeights& w, const void* a, float* Yp, hipStream_t s);
 

@@ -2,43 +2,51 @@
 // the few-token kernels take: the gate_up projection with its activation and
 // the down projection with the routing weight, over the routed positions.
 //
-// One workgroup (4 waves) computes 128 positions x 256 weight rows of one
-// expert on v_mfma_f32_32x32x16_bf16, 128 x 64 a wave, fp32 accumulators.
+// One workgroup (4 waves) computes BM = 32, 64 or 128 positions x 256 weight
+// rows of one expert on v_mfma_f32_16x16x32_bf16, BM x 64 a wave, fp32
+// accumulators.
 //
-// * The weights go from global memory straight to registers as codes: a lane
-//   holds 64 consecutive k of one weight row per 128-k stage (32 bytes, two
-//   scales), and each 8 of them become a bf16 fragment by four conversions
-//   that apply the scale (exact).  No two waves share weight rows, so LDS
-//   would only add a copy, and a wave's 128 rows of activations per converted
-//   fragment keep the conversions at a quarter of the matrix cores' time.
+// * The weights go from global memory straight to registers as codes, a whole
+//   cache line (256 k) of each of a wave's 64 rows at a time and one such line
+//   ahead.  A load covers 16 rows x 64 bytes: lane group g = lane / 16 holds
+//   block g of its row's 4 (32 x 32 tiles would take 32 rows x 32 bytes a
+//   load, which cost the loads' path twice the cache lines).  Each 8 codes
+//   become a bf16 fragment by four conversions that apply the scale (exact).
+//   No two waves share weight rows, so LDS would only add a copy.
+// * The scales of the tile's rows go to LDS before the loop, in whole runs of
+//   rows: loaded from global memory a lane a block, they touch as many cache
+//   lines as the codes do.
 // * The activations (4 times the weights' bytes per element) are shared by the
 //   4 waves through LDS, two stages of 128 k moved by buffer loads to LDS.
-//   Lane half g of a fragment takes k = 64 g + 8 q of the stage in step q,
-//   where the lane's weight codes are.
+//   Lane group g takes k 32 g + 8 q of a stage in step q, where its codes are.
 // * Rows past an expert's positions, weight rows past the matrix and k past
 //   its end are loads past their buffer's end, which give zeros.
-// * A tile's 32-row blocks without a position are skipped (the count is the
+// * A tile's 16-row blocks without a position are skipped (the count is the
 //   same for all waves), so a tile of few rows costs few products.
-// * A stage's loads are issued one stage ahead; two workgroups a CU cover each
-//   other's waits.
+// * Two or more workgroups a CU cover each other's waits.
+#include <atomic>
+#include <type_traits>
+
 #include "gemm_mx.h"
 #include "mx.h"
 
 namespace moe {
 namespace {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_vp;
 
 constexpr uint32_t kPast = 0x80000000u;   // byte offset past every buffer
 
+template <int BM_>
 struct MxCfg {
-  static constexpr int BM = 128, BN = 256, BK = 128, NW = 4, NT = NW * 64;
-  static constexpr int WTM = 128, WTN = 64, FM = 4, FN = 2;
-  static constexpr int SUB = BM * 64;   // elements of a 64-k half of a stage
-  static constexpr int NB = BM / 8 / NW;   // 1 KB loads of a wave per 64-k half (8 rows of 128 bytes)
+  static constexpr int BM = BM_, BN = 256, BK = 128, NW = 4, NT = NW * 64;
+  static constexpr int FM = BM / 16, FN = 4;   // 16 x 16 blocks of a wave: positions, weight rows
+  static constexpr int HALF = BM * 64;     // elements of a stage's 64-k half
+  static constexpr int NB = BM / 8 / NW;   // 1 KB loads of a wave per half (8 rows of 128 bytes)
+  static constexpr int OCC = BM == 32 ? 3 : 2;   // workgroups a CU that the registers allow for
 };
-using C = MxCfg;
 
 // A raw buffer of 2^31 bytes at p (wave-uniform) as its four descriptor words.
 __device__ __forceinline__ u32x4_t buffer_words(const void* p) {
@@ -67,122 +75,165 @@ __device__ __forceinline__ void dma16(u32x4_t rs, uint32_t off, uint16_t* dst) {
       : "memory", "m0");
 }
 
-// A 64-k half tile is [row][64] with 16-byte chunk c of row r at slot
+// A 64-k half is [row][64] with 16-byte chunk c of row r at slot
 // c ^ ((r / 2) % 8): 16 lanes that read one chunk of 16 consecutive rows hit
 // 16 bank groups.
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 
 // The activation rows of a tile: load j of wave w covers rows 8 (w NB + j) ..
-// +8 of a half; off[j] is this lane's row in bytes (kPast: no such row).
+// +8; off[j] is this lane's row in bytes (kPast: no such row).
+template <class C>
 struct ActRows {
   u32x4_t rs;
   uint32_t off[C::NB];
   int kc[C::NB];   // first k of this lane's chunk within a half
-  __device__ __forceinline__ void issue(int kt, int K, uint16_t* stage, int wave) const {
+  __device__ __forceinline__ void issue(int s, int K, uint16_t* stage, int wave) const {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < C::NB; ++j) {
-        const int k = kt * C::BK + h * 64 + kc[j];
-        dma16(rs, k < K && off[j] != kPast ? off[j] + 2 * k : kPast, stage + h * C::SUB + (wave * C::NB + j) * 512);
+        const int k = s * C::BK + h * 64 + kc[j];
+        dma16(rs, k < K && off[j] != kPast ? off[j] + 2 * k : kPast, stage + h * C::HALF + (wave * C::NB + j) * 512);
       }
   }
 };
 
-// The weight rows of a wave: fragment f's row lane % 32; off / soff in bytes
-// from the tile's first gate (f = 0) and up (f = 1) row, or output row.
-struct WRows {
-  __amdgpu_buffer_rsrc_t w[2], s[2];
-  uint32_t off[2], soff[2];
-};
-// One stage of a wave's weights: 64 k a lane (two 16-byte loads) and the two scales.
-// A row of an odd number of blocks ends with a lane that has one: its scale
-// comes as a byte of its own (t), so that no byte past the row is read.
-struct WStage {
-  u32x4_t c[2][2];
-  uint32_t s[2], t[2];
-};
 __device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
-__device__ __forceinline__ void load_weights(const WRows& r, int kt, int nb, int lane, WStage& st) {
-  const int b = kt * 4 + 2 * (lane >> 5);   // this lane's first block of 32 k
+
+// The weight rows of a wave, 4 groups of 16 (gate_up: gate, gate, up, up):
+// row lane % 16 of group f, off in bytes from the tile's first gate (up) row or
+// output row, sc its scales in bytes from the start of the tile's in LDS.
+struct WRows {
+  __amdgpu_buffer_rsrc_t w[2];
+  uint32_t off[4], sc[4];
+};
+// A cache line of each row: c[f][j] is the lane's block 4 j + g of the line's 8.
+struct WLine {
+  u32x4_t c[4][2];
+};
+// Groups 2 h and 2 h + 1 of line t.
+template <bool GATE_UP>
+__device__ __forceinline__ void load_line(const WRows& r, int h, int t, int nb, int lane, WLine& w) {
 #pragma unroll
-  for (int f = 0; f < 2; ++f) {
-    st.c[f][0] = load16(r.w[f], b < nb ? r.off[f] + b * 16 : kPast);
-    st.c[f][1] = load16(r.w[f], b + 1 < nb ? r.off[f] + b * 16 + 16 : kPast);
-    st.s[f] = __builtin_amdgcn_raw_buffer_load_b16(r.s[f], b + 1 < nb ? r.soff[f] + b : kPast, 0, 0);
-    st.t[f] = 0;
-    if (nb & 1) st.t[f] = __builtin_amdgcn_raw_buffer_load_b8(r.s[f], b + 1 == nb ? r.soff[f] + b : kPast, 0, 0);
-  }
+  for (int f = 2 * h; f < 2 * h + 2; ++f)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int b = t * 8 + 4 * j + (lane >> 4);
+      w.c[f][j] = load16(r.w[GATE_UP ? h : 0], b < nb ? r.off[f] + b * 16 : kPast);
+    }
 }
 
-// acc += one stage, for the tile's first NF blocks of 32 rows.
-template <int NF>
-__device__ __forceinline__ void stage_products(const uint16_t* stage, const WStage& st, f32x16 (&acc)[C::FM][C::FN],
-                                               int lane) {
-  const uint16_t* half = stage + (lane >> 5) * C::SUB;
-  const int r32 = lane & 31;
-  float sc[2][2];
+// acc += stage s (128 k), for the tile's first NF blocks of 16 positions.
+template <class C, int NF>
+__device__ __forceinline__ void stage_products(const uint16_t* stage, const uint8_t* scales, const WRows& r, const WLine& w,
+                                               int j, int s, int nb, f32x4 (&acc)[C::FM][C::FN], int lane) {
+  const int r16 = lane & 15, g = lane >> 4;
+  const uint16_t* half = stage + (g >> 1) * C::HALF;
+  const int b = min(4 * s + g, nb - 1);
+  float sc[4];
 #pragma unroll
-  for (int f = 0; f < 2; ++f) {
-    const uint32_t s = st.s[f] | st.t[f];
-    sc[f][0] = mx_scale(s & 255);
-    sc[f][1] = mx_scale(s >> 8 & 255);
-  }
+  for (int f = 0; f < 4; ++f) sc[f] = mx_scale(scales[r.sc[f] + b]);
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
+  for (int q = 0; q < 4; ++q) {
     bf16x8_t a[NF];
 #pragma unroll
     for (int i = 0; i < NF; ++i) {
-      const int row = i * 32 + r32;
-      a[i] = *(const bf16x8_t*)(half + row * 64 + ((q ^ swz(row)) << 3));
+      const int row = i * 16 + r16;
+      a[i] = *(const bf16x8_t*)(half + row * 64 + (((4 * (g & 1) + q) ^ swz(row)) << 3));
     }
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const uint32_t code = st.c[f][q >> 2][q & 3];
-      const bf16x8_t b = mx_expand(code, sc[f][q >> 2]);
+    for (int f = 0; f < 4; ++f) {
+      const bf16x8_t bw = mx_expand(w.c[f][j][q], sc[f]);
 #pragma unroll
-      for (int i = 0; i < NF; ++i) acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, a[i], acc[i][f], 0, 0, 0);
-    }
-  }
-}
-
-template <int NF>
-__device__ __forceinline__ void mainloop(const ActRows& ar, const WRows& wr, int K, uint16_t* lds,
-                                         f32x16 (&acc)[C::FM][C::FN], int wave, int lane) {
-  constexpr int STAGE = 2 * C::SUB;
-  const int nb = K >> 5, nk = (nb + 3) >> 2;
-  WStage st[2];
-  load_weights(wr, 0, nb, lane, st[0]);
-  ar.issue(0, K, lds, wave);
-  for (int kt = 0; kt < nk; kt += 2) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (kt + u < nk) {
-        __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0): the stage's own loads and the last one's reads
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (kt + u + 1 < nk) {
-          load_weights(wr, kt + u + 1, nb, lane, st[1 - u]);
-          ar.issue(kt + u + 1, K, lds + (1 - u) * STAGE, wave);
-        }
-        stage_products<NF>(lds + u * STAGE, st[u], acc, lane);
-      }
+      for (int i = 0; i < NF; ++i) acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw, a[i], acc[i][f], 0, 0, 0);
     }
   }
 }
 
-template <bool GATE_UP>
-__global__ __launch_bounds__(C::NT, 2) void mx_gemm_kernel(MxArgs p) {
-  __shared__ __align__(1024) uint16_t lds[2 * 2 * C::SUB];
+constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }   // vmcnt <= n, lgkmcnt 0
+
+// Stage s = 2 t + J: the stage's activations have landed (they were issued one
+// stage ago, before that stage's 4 weight loads, which may still be in flight)
+// and every wave is past its reads of the stage before, whose buffer the next
+// stage's loads then fill.
+template <class C, bool GATE_UP, int NF, int J>
+__device__ __forceinline__ void one_stage(const ActRows<C>& ar, const WRows& wr, const uint8_t* scales, int t, int ns, int nb,
+                                          int K, uint16_t* lds, const WLine& cur, WLine& next,
+                                          f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
+  const int s = 2 * t + J;
+  if (s >= ns) return;
+  if (s == 0) __builtin_amdgcn_s_waitcnt(wait_vm(0));
+  else __builtin_amdgcn_s_waitcnt(wait_vm(4));
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  if (s + 1 < ns) ar.issue(s + 1, K, lds + (J ^ 1) * 2 * C::HALF, wave);
+  load_line<GATE_UP>(wr, J, t + 1, nb, lane, next);
+  asm volatile("" ::: "memory");   // the loads stay here: the next stage's wait counts them
+  __builtin_amdgcn_sched_barrier(0);
+  stage_products<C, NF>(lds + J * 2 * C::HALF, scales, wr, cur, J, s, nb, acc, lane);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <class C, bool GATE_UP, int NF>
+__device__ __forceinline__ void mainloop(const ActRows<C>& ar, const WRows& wr, const uint8_t* scales, int K, uint16_t* lds,
+                                         WLine& l0, f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
+  const int nb = K >> 5, ns = (nb + 3) >> 2, nl = (nb + 7) >> 3;
+  WLine l1;
+  for (int t = 0; t < nl; t += 2) {
+    one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t, ns, nb, K, lds, l0, l1, acc, wave, lane);
+    one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t, ns, nb, K, lds, l0, l1, acc, wave, lane);
+    one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t + 1, ns, nb, K, lds, l1, l0, acc, wave, lane);
+    one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t + 1, ns, nb, K, lds, l1, l0, acc, wave, lane);
+  }
+}
+
+// `bytes` bytes (a multiple of 16) of scales at p to LDS.
+template <int NTHREADS>
+__device__ __forceinline__ void scales_to_lds(const char* p, uint32_t bytes, uint8_t* lds) {
+  const __amdgpu_buffer_rsrc_t b = buffer_of(p);
+  uint32_t o = threadIdx.x * 16;
+  for (; o + 3 * NTHREADS * 16 < bytes; o += 4 * NTHREADS * 16) {
+    u32x4_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = load16(b, o + i * NTHREADS * 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *(u32x4_t*)(lds + o + i * NTHREADS * 16) = v[i];
+  }
+  for (; o < bytes; o += NTHREADS * 16) *(u32x4_t*)(lds + o) = load16(b, o);
+}
+
+template <class C, bool GATE_UP>
+__global__ __launch_bounds__(C::NT, C::OCC) void mx_gemm_kernel(MxArgs p) {
+  extern __shared__ __align__(1024) char mx_lds[];   // two stages, then the scales
+  uint16_t* lds = (uint16_t*)mx_lds;
+  uint8_t* scales = (uint8_t*)(lds + 4 * C::HALF);
   const GArgs& g = p.g;
   int e, m0, rows, nt;
   if (!row_tile<C::BM>(g, e, m0, rows, nt)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int K = GATE_UP ? g.H : g.I;
-  ActRows ar;
+  const int K = GATE_UP ? g.H : g.I, nb = K >> 5;
+  WRows wr;
+  WLine l0;
+  // the tile's first column, its columns, and the wave's own
+  constexpr int BC = GATE_UP ? C::BN / 2 : C::BN, WC = BC / C::NW;
+  const int c0 = nt * BC, ncol = min(BC, (GATE_UP ? g.I : g.H) - c0);
+  const size_t at = GATE_UP ? (size_t)p.gu_es * e + (size_t)p.gu_rs * c0 : ((size_t)g.H * e + c0) * (size_t)(g.I / 2);
+  const uint32_t rs = GATE_UP ? (uint32_t)p.gu_rs : (uint32_t)(g.I / 2);   // bytes between columns' rows
+  const bool inter = GATE_UP && p.gu_rs != K / 2;   // gate and up rows in turn: one run of scales
+  wr.w[0] = buffer_of((const char*)(GATE_UP ? p.gu_g : p.Wd) + at);
+  wr.w[1] = buffer_of((const char*)(GATE_UP ? p.gu_u : p.Wd) + at);
+#pragma unroll
+  for (int f = 0; f < 4; ++f) {
+    const int j = min(wave * WC + (GATE_UP ? f & 1 : f) * 16 + (lane & 15), ncol - 1);
+    wr.off[f] = rs * (uint32_t)j;
+    wr.sc[f] = nb * (GATE_UP ? (inter ? 2 * j + (f >> 1) : (f >> 1) * ncol + j) : j);
+  }
+  load_line<GATE_UP>(wr, 0, 0, nb, lane, l0);
+  load_line<GATE_UP>(wr, 1, 0, nb, lane, l0);
+  ActRows<C> ar;
   ar.rs = buffer_words(GATE_UP ? g.A : (const void*)((const uint16_t*)g.A + (size_t)m0 * g.I));
 #pragma unroll
   for (int j = 0; j < C::NB; ++j) {
@@ -191,66 +242,119 @@ __global__ __launch_bounds__(C::NT, 2) void mx_gemm_kernel(MxArgs p) {
     const uint32_t r = row < rows ? (GATE_UP ? (uint32_t)g.tok_of_pos[m0 + row] : (uint32_t)row) : 0u;
     ar.off[j] = row < rows ? r * (uint32_t)(K * 2) : kPast;
   }
-  WRows wr;
-  const int n0 = GATE_UP ? nt * (C::BN / 2) + wave * 32 : nt * C::BN + wave * 64;   // the wave's first column
-#pragma unroll
-  for (int f = 0; f < 2; ++f) {
-    if (GATE_UP) {
-      const size_t at = (size_t)p.gu_es * e + (size_t)p.gu_rs * min(n0, g.I - 1);
-      const int j = min(n0 + (lane & 31), g.I - 1) - min(n0, g.I - 1);
-      wr.w[f] = buffer_of((const char*)(f ? p.gu_u : p.gu_g) + at);
-      wr.s[f] = buffer_of((const char*)(f ? p.gus_u : p.gus_g) + at / 16);
-      wr.off[f] = (uint32_t)(p.gu_rs * j);
-    } else {
-      const size_t rb = g.I / 2;
-      const size_t at = ((size_t)g.H * e + min(n0, g.H - 1)) * rb;
-      const int j = min(n0 + f * 32 + (lane & 31), g.H - 1) - min(n0, g.H - 1);
-      wr.w[f] = buffer_of((const char*)p.Wd + at);
-      wr.s[f] = buffer_of((const char*)p.sd + at / 16);
-      wr.off[f] = (uint32_t)(rb * j);
-    }
-    wr.soff[f] = wr.off[f] / 16;
+  const uint32_t run = (uint32_t)(ncol * nb);
+  if (GATE_UP) {
+    scales_to_lds<C::NT>((const char*)p.gus_g + at / 16, inter ? 2 * run : run, scales);
+    if (!inter) scales_to_lds<C::NT>((const char*)p.gus_u + at / 16, run, scales + run);
+  } else {
+    scales_to_lds<C::NT>((const char*)p.sd + at / 16, run, scales);
   }
-  f32x16 acc[C::FM][C::FN];
+  ar.issue(0, K, lds, wave);
+  f32x4 acc[C::FM][C::FN];
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-    for (int f = 0; f < C::FN; ++f)
+    for (int f = 0; f < C::FN; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int nf = (rows + 15) >> 4;
+  auto loop = [&](auto n) { mainloop<C, GATE_UP, decltype(n)::value>(ar, wr, scales, K, lds, l0, acc, wave, lane); };
+  using std::integral_constant;
+  if constexpr (C::FM == 8) {   // in steps of 32 positions: each count is code of its own
+    if (nf > 6) loop(integral_constant<int, 8>{});
+    else if (nf > 4) loop(integral_constant<int, 6>{});
+    else if (nf > 2) loop(integral_constant<int, 4>{});
+    else loop(integral_constant<int, 2>{});
+  } else {
+    if (C::FM > 3 && nf == 4) loop(integral_constant<int, C::FM>{});
+    else if (C::FM > 2 && nf == 3) loop(integral_constant<int, C::FM < 3 ? C::FM : 3>{});
+    else if (nf == 2) loop(integral_constant<int, 2>{});
+    else loop(integral_constant<int, 1>{});
+  }
+  // Accumulator element v of a lane: position 16 i + lane % 16, weight row 4
+  // (lane / 16) + v of group f.
 #pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][f][v] = 0.f;
-  const int nf = (rows + 31) >> 5;
-  if (nf > 2) mainloop<4>(ar, wr, K, lds, acc, wave, lane);
-  else if (nf == 2) mainloop<2>(ar, wr, K, lds, acc, wave, lane);
-  else mainloop<1>(ar, wr, K, lds, acc, wave, lane);
-  if (GATE_UP) epi_gate_up<C, uint16_t, true, false>(g, acc, m0, rows, nt * (C::BN / 2), 0, wave, lane);
-  else epi_down<C>(g, acc, m0, rows, nt * C::BN, 0, wave, lane);
+  for (int i = 0; i < C::FM; ++i) {
+    const int row = i * 16 + (lane & 15);
+    if (row >= rows) continue;
+    const size_t pos = (size_t)(m0 + row);
+    if constexpr (GATE_UP) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int c = wave * WC + f * 16 + 4 * (lane >> 4);
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = glu_fwd(acc[i][f][k], acc[i][2 + f][k], g.act, g.limit, g.alpha);
+        if (c < ncol) store4<uint16_t>((uint16_t*)g.out0 + pos * g.I + c0 + c, v[0], v[1], v[2], v[3]);
+      }
+    } else {
+      const float w = g.w_of_pos[pos];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int c = wave * WC + f * 16 + 4 * (lane >> 4);
+        if (c < ncol)
+          store4<float>((float*)g.out0 + pos * g.H + c0 + c, w * acc[i][f][0], w * acc[i][f][1], w * acc[i][f][2],
+                        w * acc[i][f][3]);
+      }
+    }
+  }
+}
+
+template <class C, bool GATE_UP>
+hipError_t launch(const GemmProblem& pb, MxArgs p, const char* name, hipStream_t s) {
+  constexpr int BC = GATE_UP ? C::BN / 2 : C::BN;
+  const int K = GATE_UP ? pb.H : pb.I, N = GATE_UP ? pb.I : pb.H;
+  const GArgs b = base_args(pb, C::BM);
+  p.g.offsets = b.offsets; p.g.tile_prefix = b.tile_prefix; p.g.tok_of_pos = b.tok_of_pos; p.g.w_of_pos = b.w_of_pos;
+  p.g.T = b.T; p.g.H = b.H; p.g.I = b.I; p.g.E = b.E; p.g.K = b.K; p.g.S = b.S;
+  p.g.act = b.act; p.g.layout = b.layout; p.g.limit = b.limit; p.g.alpha = b.alpha;
+  p.g.ntn = (N + BC - 1) / BC;
+  const size_t lds = 4 * C::HALF * sizeof(uint16_t) + (size_t)C::BN * (K / 32);
+  static std::atomic<uint64_t> raised{0};   // devices whose limit of dynamic LDS is raised
+  int dev = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err != hipSuccess) return err;
+  if (dev > 63 || !(raised.load() >> dev & 1)) {
+    err = hipFuncSetAttribute((const void*)mx_gemm_kernel<C, GATE_UP>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                              MX_MAX_LDS);
+    if (err != hipSuccess) return err;
+    if (dev <= 63) raised.fetch_or(uint64_t(1) << dev);
+  }
+  return run_kernel(name, s, [&] {
+    mx_gemm_kernel<C, GATE_UP><<<(int)row_grid(pb, C::BM, p.g.ntn), C::NT, lds, s>>>(p);
+  });
+}
+
+template <bool GATE_UP>
+hipError_t launch_by_rows(const GemmProblem& pb, const MxArgs& p, const char* name, hipStream_t s) {
+  switch (mx_tile_rows(pb)) {
+    case 32: return launch<MxCfg<32>, GATE_UP>(pb, p, name, s);
+    case 64: return launch<MxCfg<64>, GATE_UP>(pb, p, name, s);
+    default: return launch<MxCfg<128>, GATE_UP>(pb, p, name, s);
+  }
 }
 
 }  // namespace
 
+// Rows of a tile by the slots an expert holds on average.
+int mx_tile_rows(const GemmProblem& pb) {
+  const long mean = (long)pb.S / pb.E;
+  return mean <= 24 ? 32 : mean <= 48 ? 64 : 128;
+}
+
 hipError_t launch_mx_gate_up(const GemmProblem& pb, const MxWeights& w, const void* X, void* a, hipStream_t s) {
   MxArgs p = {};
-  p.g = base_args(pb, C::BM);
   p.g.A = X;
   p.g.out0 = a;
-  p.g.ntn = (pb.I + C::BN / 2 - 1) / (C::BN / 2);
   p.gu_g = w.gu_g; p.gu_u = w.gu_u; p.gus_g = w.gus_g; p.gus_u = w.gus_u;
   p.gu_es = w.gu_es; p.gu_rs = w.gu_rs;
-  return run_kernel("mx_gate_up", s, [&] {
-    mx_gemm_kernel<true><<<(int)row_grid(pb, C::BM, p.g.ntn), C::NT, 0, s>>>(p);
-  });
+  return launch_by_rows<true>(pb, p, "mx_gate_up", s);
 }
 
 hipError_t launch_mx_down(const GemmProblem& pb, const MxWeights& w, const void* a, float* Yp, hipStream_t s) {
   MxArgs p = {};
-  p.g = base_args(pb, C::BM);
   p.g.A = a;
   p.g.out0 = Yp;
-  p.g.ntn = (pb.H + C::BN - 1) / C::BN;
   p.Wd = w.Wd; p.sd = w.sd;
-  return run_kernel("mx_down", s, [&] {
-    mx_gemm_kernel<false><<<(int)row_grid(pb, C::BM, p.g.ntn), C::NT, 0, s>>>(p);
-  });
+  return launch_by_rows<false>(pb, p, "mx_down", s);
 }
 
 }  // namespace moe
