@@ -294,7 +294,7 @@ moe_status_t moe_mx_dequantize(const void* codes, const void* scales,
  * [E,2I,H/32] in the descriptor's gate/up layout, d_codes [E,H,I/2], d_scales
  * [E,H,I/32]; hidden, out and a = phi(..) are bf16 and products accumulate in
  * fp32.  Computes what moe_fwd computes on the weights moe_mx_dequantize
- * gives.  dtype must be MOE_BF16, H and I multiples of 32 and at most 16384,
+ * gives.  dtype must be MOE_BF16, H and I multiples of 32 and at most 14336,
  * and hidden below 2^31 bytes, else MOE_ERR_UNSUPPORTED.  ws: at least moe_mx_workspace_size() bytes.
  * Everything else as for moe_fwd (no `saved`, no backward);
  * moe_mx_fwd_logits is to it as moe_fwd_logits to moe_fwd. */

@@ -12,10 +12,10 @@ struct MxWeights {
   long gu_es, gu_rs;
 };
 
-// LDS of a CU: the tile's scales (256 rows of K / 32 bytes) and two stages of
-// activations have to fit.
+// LDS of a CU: the scales of a tile's 256 rows (K / 32 bytes each) and two
+// stages of 64 rows of activations have to fit.
 constexpr int MX_MAX_LDS = 160 * 1024;
-constexpr int MX_MAX_K = 16384;
+constexpr int MX_MAX_K = 14336;
 
 struct MxArgs {
   GArgs g;
@@ -23,7 +23,6 @@ struct MxArgs {
   long gu_es, gu_rs;
 };
 
-int mx_tile_rows(const GemmProblem& pb);
 hipError_t launch_mx_gate_up(const GemmProblem& pb, const MxWeights& w, const void* X, void* a, hipStream_t s);
 hipError_t launch_mx_down(const GemmProblem& pb, const MxWeights& w, const void* a, float* Yp, hipStream_t s);
 

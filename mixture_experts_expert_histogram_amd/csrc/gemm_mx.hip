@@ -39,13 +39,13 @@ typedef __attribute__((address_space(3))) void* lds_vp;
 
 constexpr uint32_t kPast = 0x80000000u;   // byte offset past every buffer
 
-template <int BM_>
+template <int BM_, int NW_>
 struct MxCfg {
-  static constexpr int BM = BM_, BN = 256, BK = 128, NW = 4, NT = NW * 64;
+  static constexpr int BM = BM_, NW = NW_, BN = 64 * NW, BK = 128, NT = NW * 64;
   static constexpr int FM = BM / 16, FN = 4;   // 16 x 16 blocks of a wave: positions, weight rows
   static constexpr int HALF = BM * 64;     // elements of a stage's 64-k half
   static constexpr int NB = BM / 8 / NW;   // 1 KB loads of a wave per half (8 rows of 128 bytes)
-  static constexpr int OCC = BM == 32 ? 3 : 2;   // workgroups a CU that the registers allow for
+  static constexpr int OCC = BM == 32 ? 3 : 2;   // waves a SIMD that the registers allow for
 };
 
 // A raw buffer of 2^31 bytes at p (wave-uniform) as its four descriptor words.
@@ -125,6 +125,15 @@ __device__ __forceinline__ void load_line(const WRows& r, int h, int t, int nb, 
     }
 }
 
+// Place of scale byte a in LDS: 4 bytes stay free after each 128, or the 16
+// rows of a read would hit one bank where a row has 128 scales.
+__device__ __forceinline__ uint32_t scale_at(uint32_t a) { return a + (a >> 7) * 4; }
+__device__ __forceinline__ void put_scales(uint8_t* lds, uint32_t a, u32x4_t v) {
+  uint32_t* d = (uint32_t*)(lds + scale_at(a));   // a is a multiple of 16
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = v[i];
+}
+
 // acc += stage s (128 k), for the tile's first NF blocks of 16 positions.
 template <class C, int NF>
 __device__ __forceinline__ void stage_products(const uint16_t* stage, const uint8_t* scales, const WRows& r, const WLine& w,
@@ -134,7 +143,7 @@ __device__ __forceinline__ void stage_products(const uint16_t* stage, const uint
   const int b = min(4 * s + g, nb - 1);
   float sc[4];
 #pragma unroll
-  for (int f = 0; f < 4; ++f) sc[f] = mx_scale(scales[r.sc[f] + b]);
+  for (int f = 0; f < 4; ++f) sc[f] = mx_scale(scales[scale_at(r.sc[f] + b)]);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     bf16x8_t a[NF];
@@ -190,9 +199,9 @@ __device__ __forceinline__ void mainloop(const ActRows<C>& ar, const WRows& wr, 
   }
 }
 
-// `bytes` bytes (a multiple of 16) of scales at p to LDS.
+// `bytes` bytes (a multiple of 16) of scales at p to LDS, from scale byte `to`.
 template <int NTHREADS>
-__device__ __forceinline__ void scales_to_lds(const char* p, uint32_t bytes, uint8_t* lds) {
+__device__ __forceinline__ void scales_to_lds(const char* p, uint32_t bytes, uint8_t* lds, uint32_t to) {
   const __amdgpu_buffer_rsrc_t b = buffer_of(p);
   uint32_t o = threadIdx.x * 16;
   for (; o + 3 * NTHREADS * 16 < bytes; o += 4 * NTHREADS * 16) {
@@ -200,19 +209,26 @@ __device__ __forceinline__ void scales_to_lds(const char* p, uint32_t bytes, uin
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = load16(b, o + i * NTHREADS * 16);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *(u32x4_t*)(lds + o + i * NTHREADS * 16) = v[i];
+    for (int i = 0; i < 4; ++i) put_scales(lds, to + o + i * NTHREADS * 16, v[i]);
   }
-  for (; o < bytes; o += NTHREADS * 16) *(u32x4_t*)(lds + o) = load16(b, o);
+  for (; o < bytes; o += NTHREADS * 16) put_scales(lds, to + o, load16(b, o));
 }
 
 template <class C, bool GATE_UP>
 __global__ __launch_bounds__(C::NT, C::OCC) void mx_gemm_kernel(MxArgs p) {
-  extern __shared__ __align__(1024) char mx_lds[];   // two stages, then the scales
-  uint16_t* lds = (uint16_t*)mx_lds;
+  extern __shared__ __align__(1024) char mx_dyn[];   // two stages, then the scales
+  uint16_t* lds = (uint16_t*)mx_dyn;
   uint8_t* scales = (uint8_t*)(lds + 4 * C::HALF);
   const GArgs& g = p.g;
   int e, m0, rows, nt;
   if (!row_tile<C::BM>(g, e, m0, rows, nt)) return;
+  {   // an expert's tiles share its positions evenly: one over 128 is two tiles of 65, not 128 and 1
+    const int off = g.offsets[e], n = g.offsets[e + 1] - off, tiles = (n + C::BM - 1) / C::BM;
+    const int share = ((n + tiles - 1) / tiles + 15) & ~15, mt = (m0 - off) / C::BM;
+    m0 = off + mt * share;
+    rows = min(share, n - mt * share);
+    if (rows <= 0) return;
+  }
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int K = GATE_UP ? g.H : g.I, nb = K >> 5;
   WRows wr;
@@ -244,10 +260,10 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx_gemm_kernel(MxArgs p) {
   }
   const uint32_t run = (uint32_t)(ncol * nb);
   if (GATE_UP) {
-    scales_to_lds<C::NT>((const char*)p.gus_g + at / 16, inter ? 2 * run : run, scales);
-    if (!inter) scales_to_lds<C::NT>((const char*)p.gus_u + at / 16, run, scales + run);
+    scales_to_lds<C::NT>((const char*)p.gus_g + at / 16, inter ? 2 * run : run, scales, 0);
+    if (!inter) scales_to_lds<C::NT>((const char*)p.gus_u + at / 16, run, scales, run);
   } else {
-    scales_to_lds<C::NT>((const char*)p.sd + at / 16, run, scales);
+    scales_to_lds<C::NT>((const char*)p.sd + at / 16, run, scales, 0);
   }
   ar.issue(0, K, lds, wave);
   f32x4 acc[C::FM][C::FN];
@@ -298,6 +314,13 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx_gemm_kernel(MxArgs p) {
   }
 }
 
+// Two stages, and the tile's padded scales.
+template <class C>
+constexpr size_t mx_lds(int K) {
+  const size_t sc = (size_t)C::BN * (K / 32);
+  return 4 * C::HALF * sizeof(uint16_t) + sc + (sc >> 7) * 4 + 16;
+}
+
 template <class C, bool GATE_UP>
 hipError_t launch(const GemmProblem& pb, MxArgs p, const char* name, hipStream_t s) {
   constexpr int BC = GATE_UP ? C::BN / 2 : C::BN;
@@ -307,7 +330,7 @@ hipError_t launch(const GemmProblem& pb, MxArgs p, const char* name, hipStream_t
   p.g.T = b.T; p.g.H = b.H; p.g.I = b.I; p.g.E = b.E; p.g.K = b.K; p.g.S = b.S;
   p.g.act = b.act; p.g.layout = b.layout; p.g.limit = b.limit; p.g.alpha = b.alpha;
   p.g.ntn = (N + BC - 1) / BC;
-  const size_t lds = 4 * C::HALF * sizeof(uint16_t) + (size_t)C::BN * (K / 32);
+  const size_t lds = mx_lds<C>(K);
   static std::atomic<uint64_t> raised{0};   // devices whose limit of dynamic LDS is raised
   int dev = 0;
   hipError_t err = hipGetDevice(&dev);
@@ -325,20 +348,15 @@ hipError_t launch(const GemmProblem& pb, MxArgs p, const char* name, hipStream_t
 
 template <bool GATE_UP>
 hipError_t launch_by_rows(const GemmProblem& pb, const MxArgs& p, const char* name, hipStream_t s) {
-  switch (mx_tile_rows(pb)) {
-    case 32: return launch<MxCfg<32>, GATE_UP>(pb, p, name, s);
-    case 64: return launch<MxCfg<64>, GATE_UP>(pb, p, name, s);
-    default: return launch<MxCfg<128>, GATE_UP>(pb, p, name, s);
-  }
+  const long mean = (long)pb.S / pb.E;
+  const int K = GATE_UP ? pb.H : pb.I;
+  using Big = MxCfg<128, 8>;
+  if (mean <= 24) return launch<MxCfg<32, 4>, GATE_UP>(pb, p, name, s);
+  if (mean <= 80 || mx_lds<Big>(K) > MX_MAX_LDS) return launch<MxCfg<64, 4>, GATE_UP>(pb, p, name, s);
+  return launch<Big, GATE_UP>(pb, p, name, s);
 }
 
 }  // namespace
-
-// Rows of a tile by the slots an expert holds on average.
-int mx_tile_rows(const GemmProblem& pb) {
-  const long mean = (long)pb.S / pb.E;
-  return mean <= 24 ? 32 : mean <= 48 ? 64 : 128;
-}
 
 hipError_t launch_mx_gate_up(const GemmProblem& pb, const MxWeights& w, const void* X, void* a, hipStream_t s) {
   MxArgs p = {};
