@@ -164,21 +164,21 @@ __device__ __forceinline__ void stage_products(const uint16_t* stage, const uint
 constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }   // vmcnt <= n, lgkmcnt 0
 
 // Stage s = 2 t + J: the stage's activations have landed (they were issued one
-// stage ago, before that stage's 4 weight loads, which may still be in flight)
+// stage ago, before that stage's 4 weight loads: of those the first stage of a
+// line needs the last ones itself, the second leaves them in flight; at the
+// loop's end, where some have no use and are not issued, nothing is counted on)
 // and every wave is past its reads of the stage before, whose buffer the next
-// stage's loads then fill.
-template <class C, bool GATE_UP, int NF, int J>
-__device__ __forceinline__ void one_stage(const ActRows<C>& ar, const WRows& wr, const uint8_t* scales, int t, int ns, int nb,
+// stage's loads then fill (zeros, past the last stage).
+template <class C, bool GATE_UP, int NF, int J, bool TAIL = false>
+__device__ __forceinline__ void one_stage(const ActRows<C>& ar, const WRows& wr, const uint8_t* scales, int t, int nb,
                                           int K, uint16_t* lds, const WLine& cur, WLine& next,
                                           f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
   const int s = 2 * t + J;
-  if (s >= ns) return;
-  if (s == 0) __builtin_amdgcn_s_waitcnt(wait_vm(0));
-  else __builtin_amdgcn_s_waitcnt(wait_vm(4));
+  __builtin_amdgcn_s_waitcnt(wait_vm(J == 0 || TAIL ? 0 : 4));
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  if (s + 1 < ns) ar.issue(s + 1, K, lds + (J ^ 1) * 2 * C::HALF, wave);
+  ar.issue(s + 1, K, lds + (J ^ 1) * 2 * C::HALF, wave);
   load_line<GATE_UP>(wr, J, t + 1, nb, lane, next);
   asm volatile("" ::: "memory");   // the loads stay here: the next stage's wait counts them
   __builtin_amdgcn_sched_barrier(0);
@@ -186,17 +186,31 @@ __device__ __forceinline__ void one_stage(const ActRows<C>& ar, const WRows& wr,
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// The loop's body is two lines, without a branch: with a stage skipped on some
+// path, the compiler has to take loads into a line's registers for still in
+// flight wherever they are loaded again, and waits there for everything,
+// the activations just issued among it.
 template <class C, bool GATE_UP, int NF>
 __device__ __forceinline__ void mainloop(const ActRows<C>& ar, const WRows& wr, const uint8_t* scales, int K, uint16_t* lds,
                                          WLine& l0, f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
-  const int nb = K >> 5, ns = (nb + 3) >> 2, nl = (nb + 7) >> 3;
+  const int nb = K >> 5, ns = (nb + 3) >> 2;
   WLine l1;
-  for (int t = 0; t < nl; t += 2) {
-    one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t, ns, nb, K, lds, l0, l1, acc, wave, lane);
-    one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t, ns, nb, K, lds, l0, l1, acc, wave, lane);
-    one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t + 1, ns, nb, K, lds, l1, l0, acc, wave, lane);
-    one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t + 1, ns, nb, K, lds, l1, l0, acc, wave, lane);
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));
+  int t = 0;
+  for (; 2 * t + 4 <= ns; t += 2) {
+    one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t, nb, K, lds, l0, l1, acc, wave, lane);
+    one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t, nb, K, lds, l0, l1, acc, wave, lane);
+    one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, acc, wave, lane);
+    one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, acc, wave, lane);
   }
+  if (2 * t < ns) {
+    one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t, nb, K, lds, l0, l1, acc, wave, lane);
+    if (2 * t + 1 < ns) {
+      one_stage<C, GATE_UP, NF, 1, true>(ar, wr, scales, t, nb, K, lds, l0, l1, acc, wave, lane);
+      if (2 * t + 2 < ns) one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, acc, wave, lane);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));   // no load into LDS outlives the tile
 }
 
 // `bytes` bytes (a multiple of 16) of scales at p to LDS, from scale byte `to`.
@@ -277,6 +291,10 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx_gemm_kernel(MxArgs p) {
   if constexpr (C::FM == 8) {   // in steps of 32 positions: each count is code of its own
     if (nf > 6) loop(integral_constant<int, 8>{});
     else if (nf > 4) loop(integral_constant<int, 6>{});
+    else if (nf > 2) loop(integral_constant<int, 4>{});
+    else loop(integral_constant<int, 2>{});
+  } else if constexpr (C::FM == 6) {
+    if (nf > 4) loop(integral_constant<int, 6>{});
     else if (nf > 2) loop(integral_constant<int, 4>{});
     else loop(integral_constant<int, 2>{});
   } else {
