@@ -46,6 +46,9 @@ struct MxCfg {
   static constexpr int HALF = BM * 64;     // elements of a stage's 64-k half
   static constexpr int NB = BM / 8 / NW;   // 1 KB loads of a wave per half (8 rows of 128 bytes)
   static constexpr int OCC = BM == 32 ? 3 : 2;   // waves a SIMD that the registers allow for
+  // 64-byte halves of a cache line that a weight load of a row takes at a
+  // time: with 128 positions the registers hold two halves, not two lines
+  static constexpr int LH = BM == 128 ? 1 : 2;
 };
 
 // A raw buffer of 2^31 bytes at p (wave-uniform) as its four descriptor words.
@@ -109,18 +112,20 @@ struct WRows {
   __amdgpu_buffer_rsrc_t w[2];
   uint32_t off[4], sc[4];
 };
-// A cache line of each row: c[f][j] is the lane's block 4 j + g of the line's 8.
+// A cache line of each row (LH = 2), or half of one: c[f][j] is the lane's
+// block 4 j + g of the line's 8.
+template <int LH>
 struct WLine {
-  u32x4_t c[4][2];
+  u32x4_t c[4][LH];
 };
-// Groups 2 h and 2 h + 1 of line t.
-template <bool GATE_UP>
-__device__ __forceinline__ void load_line(const WRows& r, int h, int t, int nb, int lane, WLine& w) {
+// Groups 2 h and 2 h + 1 of line (or half) t.
+template <bool GATE_UP, int LH>
+__device__ __forceinline__ void load_line(const WRows& r, int h, int t, int nb, int lane, WLine<LH>& w) {
 #pragma unroll
   for (int f = 2 * h; f < 2 * h + 2; ++f)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int b = t * 8 + 4 * j + (lane >> 4);
+    for (int j = 0; j < LH; ++j) {
+      const int b = t * 4 * LH + 4 * j + (lane >> 4);
       w.c[f][j] = load16(r.w[GATE_UP ? h : 0], b < nb ? r.off[f] + b * 16 : kPast);
     }
 }
@@ -134,30 +139,52 @@ __device__ __forceinline__ void put_scales(uint8_t* lds, uint32_t a, u32x4_t v) 
   for (int i = 0; i < 4; ++i) d[i] = v[i];
 }
 
-// acc += stage s (128 k), for the tile's first NF blocks of 16 positions.
-template <class C, int NF>
-__device__ __forceinline__ void stage_products(const uint16_t* stage, const uint8_t* scales, const WRows& r, const WLine& w,
-                                               int j, int s, int nb, f32x4 (&acc)[C::FM][C::FN], int lane) {
+// The scale bytes of stage s for the wave's 4 groups.
+__device__ __forceinline__ void read_scales(const uint8_t* scales, const WRows& r, int s, int nb, int lane, uint32_t (&sb)[4]) {
+  const int b = min(4 * s + (lane >> 4), nb - 1);
+#pragma unroll
+  for (int f = 0; f < 4; ++f) sb[f] = scales[scale_at(r.sc[f] + b)];
+}
+
+// acc += a stage (128 k), for the tile's first NF blocks of 16 positions, in
+// steps of HI blocks and 32 k: a step's activations are read from LDS one step
+// ahead, issue() (the next stage's loads) runs behind the first read, and each
+// 32 k's weights are expanded once, in their first step.  sb holds the stage's
+// scale bytes and, afterwards, the next stage's.
+template <class C, int NF, class Issue>
+__device__ __forceinline__ void stage_products(const uint16_t* stage, const uint8_t* scales, const WRows& r,
+                                               const WLine<C::LH>& w, int j, int s, int nb, uint32_t (&sb)[4],
+                                               f32x4 (&acc)[C::FM][C::FN], int lane, Issue issue) {
+  constexpr int HI = NF > 4 ? NF / 2 : NF, NH = NF / HI, STEPS = 4 * NH;
   const int r16 = lane & 15, g = lane >> 4;
   const uint16_t* half = stage + (g >> 1) * C::HALF;
-  const int b = min(4 * s + g, nb - 1);
+  bf16x8_t a[2][HI], bw[4];
+  auto read = [&](int step, bf16x8_t (&to)[HI]) {
+    const int q = step / NH, i0 = step % NH * HI;
+#pragma unroll
+    for (int i = 0; i < HI; ++i) {
+      const int row = (i0 + i) * 16 + r16;
+      to[i] = *(const bf16x8_t*)(half + row * 64 + (((4 * (g & 1) + q) ^ swz(row)) << 3));
+    }
+  };
+  read(0, a[0]);
+  issue();
   float sc[4];
 #pragma unroll
-  for (int f = 0; f < 4; ++f) sc[f] = mx_scale(scales[scale_at(r.sc[f] + b)]);
+  for (int f = 0; f < 4; ++f) sc[f] = mx_scale(sb[f]);
+  read_scales(scales, r, s + 1, nb, lane, sb);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    bf16x8_t a[NF];
-#pragma unroll
-    for (int i = 0; i < NF; ++i) {
-      const int row = i * 16 + r16;
-      a[i] = *(const bf16x8_t*)(half + row * 64 + (((4 * (g & 1) + q) ^ swz(row)) << 3));
-    }
+  for (int step = 0; step < STEPS; ++step) {
+    if (step + 1 < STEPS) read(step + 1, a[(step + 1) & 1]);
+    const int q = step / NH, i0 = step % NH * HI;
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
-      const bf16x8_t bw = mx_expand(w.c[f][j][q], sc[f]);
+      if (step % NH == 0) bw[f] = mx_expand(w.c[f][j][q], sc[f]);
 #pragma unroll
-      for (int i = 0; i < NF; ++i) acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw, a[i], acc[i][f], 0, 0, 0);
+      for (int i = 0; i < HI; ++i)
+        acc[i0 + i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[f], a[step & 1][i], acc[i0 + i][f], 0, 0, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -171,19 +198,24 @@ constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); } 
 // stage's loads then fill (zeros, past the last stage).
 template <class C, bool GATE_UP, int NF, int J, bool TAIL = false>
 __device__ __forceinline__ void one_stage(const ActRows<C>& ar, const WRows& wr, const uint8_t* scales, int t, int nb,
-                                          int K, uint16_t* lds, const WLine& cur, WLine& next,
-                                          f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
+                                          int K, uint16_t* lds, const WLine<C::LH>& cur, WLine<C::LH>& next,
+                                          uint32_t (&sb)[4], f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
   const int s = 2 * t + J;
-  __builtin_amdgcn_s_waitcnt(wait_vm(J == 0 || TAIL ? 0 : 4));
+  __builtin_amdgcn_s_waitcnt(wait_vm(J == 0 || C::LH == 1 || TAIL ? 0 : 4));
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  ar.issue(s + 1, K, lds + (J ^ 1) * 2 * C::HALF, wave);
-  load_line<GATE_UP>(wr, J, t + 1, nb, lane, next);
-  asm volatile("" ::: "memory");   // the loads stay here: the next stage's wait counts them
-  __builtin_amdgcn_sched_barrier(0);
-  stage_products<C, NF>(lds + J * 2 * C::HALF, scales, wr, cur, J, s, nb, acc, lane);
-  __builtin_amdgcn_sched_barrier(0);
+  stage_products<C, NF>(lds + J * 2 * C::HALF, scales, wr, cur, C::LH == 2 ? J : 0, s, nb, sb, acc, lane, [&] {
+    ar.issue(s + 1, K, lds + (J ^ 1) * 2 * C::HALF, wave);
+    if constexpr (C::LH == 2) {
+      load_line<GATE_UP>(wr, J, t + 1, nb, lane, next);
+    } else {
+      load_line<GATE_UP>(wr, 0, s + 1, nb, lane, next);
+      load_line<GATE_UP>(wr, 1, s + 1, nb, lane, next);
+    }
+    asm volatile("" ::: "memory");   // the loads stay here: the next stage's wait counts them
+    __builtin_amdgcn_sched_barrier(0);
+  });
 }
 
 // The loop's body is two lines, without a branch: with a stage skipped on some
@@ -192,22 +224,35 @@ __device__ __forceinline__ void one_stage(const ActRows<C>& ar, const WRows& wr,
 // the activations just issued among it.
 template <class C, bool GATE_UP, int NF>
 __device__ __forceinline__ void mainloop(const ActRows<C>& ar, const WRows& wr, const uint8_t* scales, int K, uint16_t* lds,
-                                         WLine& l0, f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
+                                         WLine<C::LH>& l0, f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
   const int nb = K >> 5, ns = (nb + 3) >> 2;
-  WLine l1;
+  WLine<C::LH> l1;
+  uint32_t sb[4];
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();   // every wave's scales are in LDS
+  asm volatile("" ::: "memory");
+  read_scales(scales, wr, 0, nb, lane, sb);
   int t = 0;
-  for (; 2 * t + 4 <= ns; t += 2) {
-    one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t, nb, K, lds, l0, l1, acc, wave, lane);
-    one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t, nb, K, lds, l0, l1, acc, wave, lane);
-    one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, acc, wave, lane);
-    one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, acc, wave, lane);
-  }
-  if (2 * t < ns) {
-    one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t, nb, K, lds, l0, l1, acc, wave, lane);
-    if (2 * t + 1 < ns) {
-      one_stage<C, GATE_UP, NF, 1, true>(ar, wr, scales, t, nb, K, lds, l0, l1, acc, wave, lane);
-      if (2 * t + 2 < ns) one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, acc, wave, lane);
+  if constexpr (C::LH == 1) {
+    for (; 2 * t + 2 <= ns; ++t) {
+      one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
+      one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t, nb, K, lds, l1, l0, sb, acc, wave, lane);
+    }
+    if (2 * t < ns) one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
+  } else {
+    for (; 2 * t + 4 <= ns; t += 2) {
+      one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
+      one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
+      one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, sb, acc, wave, lane);
+      one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, sb, acc, wave, lane);
+    }
+    if (2 * t < ns) {
+      one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
+      if (2 * t + 1 < ns) {
+        one_stage<C, GATE_UP, NF, 1, true>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
+        if (2 * t + 2 < ns) one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, sb, acc, wave, lane);
+      }
     }
   }
   __builtin_amdgcn_s_waitcnt(wait_vm(0));   // no load into LDS outlives the tile
@@ -246,7 +291,7 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx_gemm_kernel(MxArgs p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int K = GATE_UP ? g.H : g.I, nb = K >> 5;
   WRows wr;
-  WLine l0;
+  WLine<C::LH> l0;
   // the tile's first column, its columns, and the wave's own
   constexpr int BC = GATE_UP ? C::BN / 2 : C::BN, WC = BC / C::NW;
   const int c0 = nt * BC, ncol = min(BC, (GATE_UP ? g.I : g.H) - c0);
