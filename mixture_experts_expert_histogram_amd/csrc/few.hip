@@ -274,7 +274,7 @@ template <> struct Elem<W_F32> { using T = float; };
 template <int KIND> struct Tune;
 template <> struct Tune<W_BF16> { static constexpr int G = 2, D1 = 2, D2 = 1, NW = 4, OCC = 4, NT2 = 2; };
 template <> struct Tune<W_F32> { static constexpr int G = 2, D1 = 2, D2 = 1, NW = 4, OCC = 4, NT2 = 2; };
-template <> struct Tune<W_MX> { static constexpr int G = 4, D1 = 1, D2 = 1, NW = 4, OCC = 4, NT2 = 1; };
+template <> struct Tune<W_MX> { static constexpr int G = 4, D1 = 1, D2 = 1, NW = 4, OCC = 3, NT2 = 2; };
 
 // Rows of G/2 gate and up groups: groups 2i and 2i+1 are the gate and up rows
 // of activation columns j0 + 16 i .. +15.

@@ -173,6 +173,7 @@ __device__ __forceinline__ void stage_products(const uint16_t* stage, const uint
 #pragma unroll
   for (int f = 0; f < 4; ++f) sc[f] = mx_scale(sb[f]);
   read_scales(scales, r, s + 1, nb, lane, sb);
+  __builtin_amdgcn_s_setprio(1);
 #pragma unroll
   for (int step = 0; step < STEPS; ++step) {
     if (step + 1 < STEPS) read(step + 1, a[(step + 1) & 1]);
@@ -186,6 +187,7 @@ __device__ __forceinline__ void stage_products(const uint16_t* stage, const uint
     }
     __builtin_amdgcn_sched_barrier(0);
   }
+  __builtin_amdgcn_s_setprio(0);
 }
 
 constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }   // vmcnt <= n, lgkmcnt 0
@@ -356,22 +358,26 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx_gemm_kernel(MxArgs p) {
     if (row >= rows) continue;
     const size_t pos = (size_t)(m0 + row);
     if constexpr (GATE_UP) {
+      uint32_t d[2][2];   // the 16 columns of group f, 4 a lane
 #pragma unroll
       for (int f = 0; f < 2; ++f) {
-        const int c = wave * WC + f * 16 + 4 * (lane >> 4);
         float v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = glu_fwd(acc[i][f][k], acc[i][2 + f][k], g.act, g.limit, g.alpha);
-        if (c < ncol) store4<uint16_t>((uint16_t*)g.out0 + pos * g.I + c0 + c, v[0], v[1], v[2], v[3]);
+        d[f][0] = pack_bf16(v[0], v[1]);
+        d[f][1] = pack_bf16(v[2], v[3]);
       }
+      // lanes of even 16s take their and the next 16s' columns of group 0, the others of group 1: 16 bytes each
+      const auto x = __builtin_amdgcn_permlane16_swap(d[0][0], d[1][0], false, false);
+      const auto y = __builtin_amdgcn_permlane16_swap(d[0][1], d[1][1], false, false);
+      const int c = wave * WC + ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
+      if (c < ncol) *(u32x4_t*)((uint16_t*)g.out0 + pos * g.I + c0 + c) = u32x4_t{x[0], y[0], x[1], y[1]};
     } else {
       const float w = g.w_of_pos[pos];
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
         const int c = wave * WC + f * 16 + 4 * (lane >> 4);
-        if (c < ncol)
-          store4<float>((float*)g.out0 + pos * g.H + c0 + c, w * acc[i][f][0], w * acc[i][f][1], w * acc[i][f][2],
-                        w * acc[i][f][3]);
+        if (c < ncol) *(f32x4*)((float*)g.out0 + pos * g.H + c0 + c) = w * acc[i][f];
       }
     }
   }
