@@ -2,7 +2,7 @@
 // the few-token kernels take: the gate_up projection with its activation and
 // the down projection with the routing weight, over the routed positions.
 //
-// One workgroup (4 waves) computes BM = 32, 64 or 128 positions x 256 weight
+// One workgroup (4 waves) computes BM = 32 or 64 positions x 256 weight
 // rows of one expert on v_mfma_f32_16x16x32_bf16, BM x 64 a wave, fp32
 // accumulators.
 //
@@ -39,16 +39,13 @@ typedef __attribute__((address_space(3))) void* lds_vp;
 
 constexpr uint32_t kPast = 0x80000000u;   // byte offset past every buffer
 
-template <int BM_, int NW_>
+template <int BM_>
 struct MxCfg {
-  static constexpr int BM = BM_, NW = NW_, BN = 64 * NW, BK = 128, NT = NW * 64;
+  static constexpr int BM = BM_, BN = 256, BK = 128, NW = 4, NT = NW * 64;
   static constexpr int FM = BM / 16, FN = 4;   // 16 x 16 blocks of a wave: positions, weight rows
   static constexpr int HALF = BM * 64;     // elements of a stage's 64-k half
   static constexpr int NB = BM / 8 / NW;   // 1 KB loads of a wave per half (8 rows of 128 bytes)
   static constexpr int OCC = BM == 32 ? 3 : 2;   // waves a SIMD that the registers allow for
-  // 64-byte halves of a cache line that a weight load of a row takes at a
-  // time: with 128 positions the registers hold two halves, not two lines
-  static constexpr int LH = BM == 128 ? 1 : 2;
 };
 
 // A raw buffer of 2^31 bytes at p (wave-uniform) as its four descriptor words.
@@ -112,20 +109,18 @@ struct WRows {
   __amdgpu_buffer_rsrc_t w[2];
   uint32_t off[4], sc[4];
 };
-// A cache line of each row (LH = 2), or half of one: c[f][j] is the lane's
-// block 4 j + g of the line's 8.
-template <int LH>
+// A cache line of each row: c[f][j] is the lane's block 4 j + g of the line's 8.
 struct WLine {
-  u32x4_t c[4][LH];
+  u32x4_t c[4][2];
 };
-// Groups 2 h and 2 h + 1 of line (or half) t.
-template <bool GATE_UP, int LH>
-__device__ __forceinline__ void load_line(const WRows& r, int h, int t, int nb, int lane, WLine<LH>& w) {
+// Groups 2 h and 2 h + 1 of line t.
+template <bool GATE_UP>
+__device__ __forceinline__ void load_line(const WRows& r, int h, int t, int nb, int lane, WLine& w) {
 #pragma unroll
   for (int f = 2 * h; f < 2 * h + 2; ++f)
 #pragma unroll
-    for (int j = 0; j < LH; ++j) {
-      const int b = t * 4 * LH + 4 * j + (lane >> 4);
+    for (int j = 0; j < 2; ++j) {
+      const int b = t * 8 + 4 * j + (lane >> 4);
       w.c[f][j] = load16(r.w[GATE_UP ? h : 0], b < nb ? r.off[f] + b * 16 : kPast);
     }
 }
@@ -147,23 +142,20 @@ __device__ __forceinline__ void read_scales(const uint8_t* scales, const WRows& 
 }
 
 // acc += a stage (128 k), for the tile's first NF blocks of 16 positions, in
-// steps of HI blocks and 32 k: a step's activations are read from LDS one step
-// ahead, issue() (the next stage's loads) runs behind the first read, and each
-// 32 k's weights are expanded once, in their first step.  sb holds the stage's
-// scale bytes and, afterwards, the next stage's.
+// steps of 32 k: a step's activations are read from LDS one step ahead, and
+// issue() (the next stage's loads) runs behind the first read.  sb holds the
+// stage's scale bytes and, afterwards, the next stage's.
 template <class C, int NF, class Issue>
 __device__ __forceinline__ void stage_products(const uint16_t* stage, const uint8_t* scales, const WRows& r,
-                                               const WLine<C::LH>& w, int j, int s, int nb, uint32_t (&sb)[4],
+                                               const WLine& w, int j, int s, int nb, uint32_t (&sb)[4],
                                                f32x4 (&acc)[C::FM][C::FN], int lane, Issue issue) {
-  constexpr int HI = NF > 4 ? NF / 2 : NF, NH = NF / HI, STEPS = 4 * NH;
   const int r16 = lane & 15, g = lane >> 4;
   const uint16_t* half = stage + (g >> 1) * C::HALF;
-  bf16x8_t a[2][HI], bw[4];
-  auto read = [&](int step, bf16x8_t (&to)[HI]) {
-    const int q = step / NH, i0 = step % NH * HI;
+  bf16x8_t a[2][NF];
+  auto read = [&](int q, bf16x8_t (&to)[NF]) {
 #pragma unroll
-    for (int i = 0; i < HI; ++i) {
-      const int row = (i0 + i) * 16 + r16;
+    for (int i = 0; i < NF; ++i) {
+      const int row = i * 16 + r16;
       to[i] = *(const bf16x8_t*)(half + row * 64 + (((4 * (g & 1) + q) ^ swz(row)) << 3));
     }
   };
@@ -175,15 +167,14 @@ __device__ __forceinline__ void stage_products(const uint16_t* stage, const uint
   read_scales(scales, r, s + 1, nb, lane, sb);
   __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-  for (int step = 0; step < STEPS; ++step) {
-    if (step + 1 < STEPS) read(step + 1, a[(step + 1) & 1]);
-    const int q = step / NH, i0 = step % NH * HI;
+  for (int q = 0; q < 4; ++q) {
+    if (q < 3) read(q + 1, a[(q + 1) & 1]);
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
-      if (step % NH == 0) bw[f] = mx_expand(w.c[f][j][q], sc[f]);
+      const bf16x8_t bw = mx_expand(w.c[f][j][q], sc[f]);
 #pragma unroll
-      for (int i = 0; i < HI; ++i)
-        acc[i0 + i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw[f], a[step & 1][i], acc[i0 + i][f], 0, 0, 0);
+      for (int i = 0; i < NF; ++i)
+        acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bw, a[q & 1][i], acc[i][f], 0, 0, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -200,21 +191,16 @@ constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); } 
 // stage's loads then fill (zeros, past the last stage).
 template <class C, bool GATE_UP, int NF, int J, bool TAIL = false>
 __device__ __forceinline__ void one_stage(const ActRows<C>& ar, const WRows& wr, const uint8_t* scales, int t, int nb,
-                                          int K, uint16_t* lds, const WLine<C::LH>& cur, WLine<C::LH>& next,
+                                          int K, uint16_t* lds, const WLine& cur, WLine& next,
                                           uint32_t (&sb)[4], f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
   const int s = 2 * t + J;
-  __builtin_amdgcn_s_waitcnt(wait_vm(J == 0 || C::LH == 1 || TAIL ? 0 : 4));
+  __builtin_amdgcn_s_waitcnt(wait_vm(J == 0 || TAIL ? 0 : 4));
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  stage_products<C, NF>(lds + J * 2 * C::HALF, scales, wr, cur, C::LH == 2 ? J : 0, s, nb, sb, acc, lane, [&] {
+  stage_products<C, NF>(lds + J * 2 * C::HALF, scales, wr, cur, J, s, nb, sb, acc, lane, [&] {
     ar.issue(s + 1, K, lds + (J ^ 1) * 2 * C::HALF, wave);
-    if constexpr (C::LH == 2) {
-      load_line<GATE_UP>(wr, J, t + 1, nb, lane, next);
-    } else {
-      load_line<GATE_UP>(wr, 0, s + 1, nb, lane, next);
-      load_line<GATE_UP>(wr, 1, s + 1, nb, lane, next);
-    }
+    load_line<GATE_UP>(wr, J, t + 1, nb, lane, next);
     asm volatile("" ::: "memory");   // the loads stay here: the next stage's wait counts them
     __builtin_amdgcn_sched_barrier(0);
   });
@@ -226,9 +212,9 @@ __device__ __forceinline__ void one_stage(const ActRows<C>& ar, const WRows& wr,
 // the activations just issued among it.
 template <class C, bool GATE_UP, int NF>
 __device__ __forceinline__ void mainloop(const ActRows<C>& ar, const WRows& wr, const uint8_t* scales, int K, uint16_t* lds,
-                                         WLine<C::LH>& l0, f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
+                                         WLine& l0, f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
   const int nb = K >> 5, ns = (nb + 3) >> 2;
-  WLine<C::LH> l1;
+  WLine l1;
   uint32_t sb[4];
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
   asm volatile("" ::: "memory");
@@ -236,25 +222,17 @@ __device__ __forceinline__ void mainloop(const ActRows<C>& ar, const WRows& wr, 
   asm volatile("" ::: "memory");
   read_scales(scales, wr, 0, nb, lane, sb);
   int t = 0;
-  if constexpr (C::LH == 1) {
-    for (; 2 * t + 2 <= ns; ++t) {
-      one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
-      one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t, nb, K, lds, l1, l0, sb, acc, wave, lane);
-    }
-    if (2 * t < ns) one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
-  } else {
-    for (; 2 * t + 4 <= ns; t += 2) {
-      one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
-      one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
-      one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, sb, acc, wave, lane);
-      one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, sb, acc, wave, lane);
-    }
-    if (2 * t < ns) {
-      one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
-      if (2 * t + 1 < ns) {
-        one_stage<C, GATE_UP, NF, 1, true>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
-        if (2 * t + 2 < ns) one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, sb, acc, wave, lane);
-      }
+  for (; 2 * t + 4 <= ns; t += 2) {
+    one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
+    one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
+    one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, sb, acc, wave, lane);
+    one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, sb, acc, wave, lane);
+  }
+  if (2 * t < ns) {
+    one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
+    if (2 * t + 1 < ns) {
+      one_stage<C, GATE_UP, NF, 1, true>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
+      if (2 * t + 2 < ns) one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, sb, acc, wave, lane);
     }
   }
   __builtin_amdgcn_s_waitcnt(wait_vm(0));   // no load into LDS outlives the tile
@@ -293,7 +271,7 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx_gemm_kernel(MxArgs p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int K = GATE_UP ? g.H : g.I, nb = K >> 5;
   WRows wr;
-  WLine<C::LH> l0;
+  WLine l0;
   // the tile's first column, its columns, and the wave's own
   constexpr int BC = GATE_UP ? C::BN / 2 : C::BN, WC = BC / C::NW;
   const int c0 = nt * BC, ncol = min(BC, (GATE_UP ? g.I : g.H) - c0);
@@ -335,19 +313,13 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx_gemm_kernel(MxArgs p) {
   const int nf = (rows + 15) >> 4;
   auto loop = [&](auto n) { mainloop<C, GATE_UP, decltype(n)::value>(ar, wr, scales, K, lds, l0, acc, wave, lane); };
   using std::integral_constant;
-  if constexpr (C::FM == 8) {   // in steps of 32 positions: each count is code of its own
-    if (nf > 6) loop(integral_constant<int, 8>{});
-    else if (nf > 4) loop(integral_constant<int, 6>{});
-    else if (nf > 2) loop(integral_constant<int, 4>{});
-    else loop(integral_constant<int, 2>{});
-  } else if constexpr (C::FM == 6) {
-    if (nf > 4) loop(integral_constant<int, 6>{});
-    else if (nf > 2) loop(integral_constant<int, 4>{});
-    else loop(integral_constant<int, 2>{});
-  } else {
-    if (C::FM > 3 && nf == 4) loop(integral_constant<int, C::FM>{});
-    else if (C::FM > 2 && nf == 3) loop(integral_constant<int, C::FM < 3 ? C::FM : 3>{});
+  if constexpr (C::FM == 4) {
+    if (nf == 4) loop(integral_constant<int, 4>{});
+    else if (nf == 3) loop(integral_constant<int, 3>{});
     else if (nf == 2) loop(integral_constant<int, 2>{});
+    else loop(integral_constant<int, 1>{});
+  } else {
+    if (nf == 2) loop(integral_constant<int, 2>{});
     else loop(integral_constant<int, 1>{});
   }
   // Accumulator element v of a lane: position 16 i + lane % 16, weight row 4
@@ -415,14 +387,17 @@ hipError_t launch(const GemmProblem& pb, MxArgs p, const char* name, hipStream_t
   });
 }
 
+// Tiles of 32 positions for experts of at most 16 on average, where reading
+// the weights is all of the time (more workgroups a CU: gpt-oss-shaped layer at
+// 256 tokens, 8 an expert, 402 us against 413; at 512 both 442), else of 64
+// (1024 tokens 503 us against 516, 4096 tokens 1.00 ms against 1.14).  Tiles of
+// 128 positions x 512 rows on 8 waves move a third less through the load path,
+// but one workgroup a CU leaves its waits and its ends uncovered: 1.01 ms at
+// 4096 tokens, 3.32 against 3.37 ms at 16384.
 template <bool GATE_UP>
 hipError_t launch_by_rows(const GemmProblem& pb, const MxArgs& p, const char* name, hipStream_t s) {
-  const long mean = (long)pb.S / pb.E;
-  const int K = GATE_UP ? pb.H : pb.I;
-  using Big = MxCfg<128, 8>;
-  if (mean <= 24) return launch<MxCfg<32, 4>, GATE_UP>(pb, p, name, s);
-  if (mean <= 80 || mx_lds<Big>(K) > MX_MAX_LDS) return launch<MxCfg<64, 4>, GATE_UP>(pb, p, name, s);
-  return launch<Big, GATE_UP>(pb, p, name, s);
+  if ((long)pb.S <= 16L * pb.E) return launch<MxCfg<32>, GATE_UP>(pb, p, name, s);
+  return launch<MxCfg<64>, GATE_UP>(pb, p, name, s);
 }
 
 }  // namespace

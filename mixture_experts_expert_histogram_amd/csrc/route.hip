@@ -39,20 +39,26 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_hist_kernel(
   if (threadIdx.x == 0) blk_bad[blockIdx.x] = bad;
 }
 
-// Exclusive scan over one value per thread of a 1024-thread block.
+// Exclusive scan over one value per thread of a 1024-thread block, by shuffles
+// inside each wavefront and the 16 wavefronts' totals in LDS (two barriers a
+// scan instead of 22: the routing scan makes nine of them, which took most of
+// its time).  sh[1023] holds the block's total until the next scan.
 __device__ int block_exclusive_scan_1024(int v, int* sh) {
-  const int t = threadIdx.x;
-  sh[t] = v;
-  __syncthreads();
-  for (int d = 1; d < 1024; d <<= 1) {
-    int add = (t >= d) ? sh[t - d] : 0;
-    __syncthreads();
-    sh[t] += add;
-    __syncthreads();
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  int incl = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(incl, d);
+    if (lane >= d) incl += o;
   }
-  int incl = sh[t];
+  if (lane == 63) sh[wave] = incl;
   __syncthreads();
-  return incl - v;
+  int base = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) base += w < wave ? sh[w] : 0;
+  if (t == 1023) sh[1023] = base + incl;
+  __syncthreads();
+  return base + incl - v;
 }
 
 // Pass 2 (one workgroup): counts, offsets, per-chunk bases, M-tile tables,
