@@ -252,6 +252,8 @@ moe_status_t moe_fwd_noalloc(const moe_desc_t* desc, const void* hidden,
  * by kernels sized for one or two slots an expert.  a = phi(..) is rounded to
  * the activations' type as in moe_fwd; sums over H, I and K are fp32 in a fixed
  * order (not moe_fwd's order, so the two agree to rounding, not bit for bit).
+ * Where a large bf16 layer's experts hold more than 32 slots on average it
+ * runs moe_fwd's kernels instead, which are then faster.
  * MOE_ERR_UNSUPPORTED also where 64 rows of the weights, hidden, or a [S,I]
  * reach 2^31 bytes.  ws: at least moe_few_workspace_size() bytes (its first
  * word is the status that moe_check_device_status reports); nothing in it has

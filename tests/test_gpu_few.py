@@ -62,6 +62,12 @@ def test_one_expert_takes_every_token(T, dtype):
     run_case(inp)
 
 
+@pytest.mark.parametrize("T", [32, 33, 128])
+def test_large_layer_of_few_experts(T):
+    """Sizes on both sides of the rule that hands a call to the forward's kernels (32 slots an expert, H I of 2^21)."""
+    run_case(small_inputs(T, 1456, 1456, 2, 2, "bf16", "clamped", "interleaved", seed=T))
+
+
 def test_repeated_ids_of_one_token():
     """Every slot of every token on one expert: 8 slots a token, 128 x 8 on the expert."""
     ids = np.full((128, 8), 1, dtype=np.int32)

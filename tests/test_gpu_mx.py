@@ -142,6 +142,19 @@ def test_one_expert_takes_every_token(T):
     mx_case(small_inputs(T, 288, 160, 4, 1, "bf16", "clamped", "concat", seed=T, ids=ids))
 
 
+@pytest.mark.parametrize("T", [32, 33, 128])
+def test_large_layer_of_few_experts(T):
+    """Sizes on both sides of the rule between the few-token kernels and the grouped products."""
+    mx_case(small_inputs(T, 1472, 1472, 2, 2, "bf16", "swiglu", "concat", seed=T))
+
+
+@pytest.mark.parametrize("T", [3, 140])
+def test_long_rows(T):
+    """Rows of many scales: past the few-token kernels' limit of 8192, and the longest ones."""
+    for H, I in ((8224, 32), (32, 8224), (14336, 32), (32, 14336)):
+        mx_case(small_inputs(T, H, I, 2, 1, "bf16", "swiglu", "interleaved", seed=T))
+
+
 @pytest.mark.parametrize("T", [4, 200])
 def test_bad_ids_are_dropped_and_reported(T):
     E = 5
