@@ -481,9 +481,11 @@ moe_status_t mx_check(const Dims& d) {
 }
 
 // Whether the 4-bit layer runs on the few-token kernels.
-// Those hold a workgroup's scales in LDS: rows of at most 8192.
+// Those hold an expert's slots and a workgroup's scales in LDS, beside 32 KB of
+// partial sums, within 64 KB.
 bool mx_few(const Dims& d) {
-  return few_check(d) == MOE_OK && d.H <= 8192 && d.I <= 8192 && !many_slots(d);
+  const int64_t wide = d.H > d.I ? d.H : d.I;
+  return few_check(d) == MOE_OK && wide <= 8192 && 2 * d.S + 2 * wide <= 31 * 1024 && !many_slots(d);
 }
 size_t mx_ws(const Dims& d) { return mx_few(d) ? few_layout(d).end : make_layout(d).f_end; }
 

@@ -65,7 +65,8 @@ def check_layer(got, ref, bound, name=""):
 def quantize_ref(w):
     """(codes, scale bytes) one an element / block of 32, in fp64: the format's
     definition, by search over the eight magnitudes."""
-    x = np.asarray(w, dtype=np.float64).reshape(-1, 32)
+    with np.errstate(invalid="ignore"):   # signalling NaNs
+        x = np.asarray(w, dtype=np.float64).reshape(-1, 32)
     codes = np.zeros(x.shape, dtype=np.uint8)
     scales = np.zeros(len(x), dtype=np.uint8)
     for b, row in enumerate(x):

@@ -54,6 +54,40 @@ def test_expert_counts(E, K):
     run_case(small_inputs(4, 64, 40, E, K, "bf16", "swiglu", "interleaved", seed=E))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("K", [1, 2, 3, 5, 8, 16, 17, 64])
+def test_one_token(K, dtype):
+    """One token's own kernels: fewer, as many and more slots than waves, and bad ids among them."""
+    run_case(small_inputs(1, 136, 72, 64, K, dtype, "clamped", "interleaved", seed=K))
+    run_case(small_inputs(1, 72, 200, 64, K, dtype, "swiglu", "concat", seed=K))
+    ids = np.resize(np.array([3, -1, 3, 64, 5], dtype=np.int32), (1, K))
+    got, ws = run_case(small_inputs(1, 40, 24, 64, K, dtype, "swiglu", "concat", seed=K, ids=ids))
+    assert moe.check_device_status(ws) == (moe.MOE_ERR_BAD_EXPERT_ID if K > 1 else moe.MOE_OK)
+
+
+@pytest.mark.parametrize("E", [1, 2, 5, 63, 64, 129, 1024])
+def test_one_token_from_logits(E):
+    """The choice inside one token's kernel is the router's: ties, infinities, NaN."""
+    K = min(E, 6)
+    inp = small_inputs(1, 64, 40, E, K, "bf16", "swiglu", "concat", seed=E)
+    d = device_inputs(inp)
+    g = torch.Generator().manual_seed(E)
+    rows = [torch.randn(1, E, generator=g), torch.randint(0, 3, (1, E), generator=g).float(), torch.zeros(1, E),
+            torch.full((1, E), float("-inf"))]
+    nan = torch.randn(1, E, generator=g)
+    nan[0, ::2] = float("nan")
+    rows += [nan, torch.full((1, E), float("nan"))]
+    for lg in rows:
+        lg = lg.cuda()
+        out, ids, w, ws = moe.fwd_few_logits(d["hidden"], lg, K, d["w_gate_up"], d["w_down"])
+        rids, rw, *_, rws = moe.router(lg, K)
+        assert torch.equal(ids, rids)
+        assert torch.equal(w.view(torch.int32), rw.view(torch.int32)) or torch.equal(torch.isnan(w), torch.isnan(rw))
+        assert moe.check_device_status(ws) == moe.check_device_status(rws)
+        if torch.all(torch.isfinite(w)):
+            assert torch.equal(out, moe.fwd_few(d["hidden"], ids, w, d["w_gate_up"], d["w_down"])[0])
+
+
 @pytest.mark.parametrize("T", [16, 17, 32, 33, 65, 128])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_one_expert_takes_every_token(T, dtype):
@@ -198,3 +232,58 @@ def test_full_size_layer():
     ref, bound = layer_bound(host(x), ids.cpu().numpy(), host(w), [used.get(e, none) for e in range(E)], "clamped", "interleaved",
                              "bf16")
     check_layer(host(out), ref, bound)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, with workspaces of their own."""
+    cases = [small_inputs(T, 512, 256, 16, 4, "bf16", "swiglu", "concat", seed=T) for T in (3, 40)]
+    dev = [device_inputs(c) for c in cases]
+    args = [(d["hidden"], d["topk_ids"], d["topk_weights"], d["w_gate_up"], d["w_down"]) for d in dev]
+    want = [moe.fwd_few(*a)[0] for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(moe.fwd_few(*args[i])[0])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+def test_refusals_of_the_binding():
+    inp = small_inputs(4, 64, 32, 4, 2, "bf16", "swiglu", "concat")
+    d = device_inputs(inp)
+    x, ids, w, gu, dn = d["hidden"], d["topk_ids"], d["topk_weights"], d["w_gate_up"], d["w_down"]
+    for bad in [(x.t().contiguous().t(), ids, w, gu, dn), (x.float(), ids, w, gu, dn), (x.half(), ids, w, gu.half(), dn.half()),
+                (x, ids, w, gu[:, :, :32], dn), (x, ids[:2], w, gu, dn), (x, ids, w[:, :1], gu, dn),
+                (x, ids, w, gu.transpose(1, 2), dn), (x, ids.cpu(), w, gu, dn), (x, ids, w, gu, dn.cpu()), (x[0], ids, w, gu, dn)]:
+        with pytest.raises(ValueError):
+            moe.fwd_few(*bad)
+    for kw in (dict(act="gelu"), dict(layout="rows"), dict(out=torch.empty(4, 64, device="cuda")),
+               dict(out=torch.empty(4, 64, dtype=torch.bfloat16)), dict(ws=torch.empty(1 << 20, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            moe.fwd_few(x, ids, w, gu, dn, **kw)
+    with pytest.raises(moe.MoeError) as e:
+        moe.fwd_few(x, ids, w, gu, dn, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == moe.MOE_ERR_WORKSPACE
+    many = torch.zeros(129, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(moe.MoeError) as e:
+        moe.fwd_few(many, torch.zeros(129, 2, dtype=torch.int32, device="cuda"), torch.ones(129, 2, device="cuda"), gu, dn)
+    assert e.value.status == moe.MOE_ERR_UNSUPPORTED
+    with pytest.raises(ValueError):
+        moe.fwd_few_logits(x, torch.zeros(4, 5, device="cuda"), 2, gu, dn)
+    with pytest.raises(moe.MoeError) as e:
+        moe.fwd_few_logits(x, torch.zeros(4, 4, device="cuda"), 5, gu, dn)
+    assert e.value.status == moe.MOE_ERR_INVALID_ARG
+
+
+def test_other_id_and_weight_types():
+    """64-bit ids and half-precision weights are converted; an out tensor of the caller's is filled."""
+    inp = small_inputs(4, 64, 32, 4, 2, "bf16", "swiglu", "concat")
+    d = device_inputs(inp)
+    want, _ = moe.fwd_few(d["hidden"], d["topk_ids"], d["topk_weights"].bfloat16().float(), d["w_gate_up"], d["w_down"])
+    out = torch.empty_like(want)
+    got, _ = moe.fwd_few(d["hidden"], d["topk_ids"].long(), d["topk_weights"].bfloat16(), d["w_gate_up"], d["w_down"], out=out)
+    assert got is out and torch.equal(got, want)

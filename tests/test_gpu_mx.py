@@ -155,6 +155,37 @@ def test_long_rows(T):
         mx_case(small_inputs(T, H, I, 2, 1, "bf16", "swiglu", "interleaved", seed=T))
 
 
+@pytest.mark.parametrize("K", [1, 2, 3, 5, 8, 9, 17, 64])
+def test_one_token(K):
+    """One token's own kernels: fewer, as many and more slots than waves."""
+    mx_case(small_inputs(1, 288, 160, 64, K, "bf16", "clamped", "interleaved", seed=K))
+    mx_case(small_inputs(1, 160, 288, 64, K, "bf16", "swiglu", "concat", seed=K))
+    ids = np.resize(np.array([3, -1, 3, 64, 5], dtype=np.int32), (1, K))
+    got, ws = mx_case(small_inputs(1, 96, 64, 64, K, "bf16", "swiglu", "concat", seed=K, ids=ids))
+    assert moe.check_device_status(ws) == (moe.MOE_ERR_BAD_EXPERT_ID if K > 1 else moe.MOE_OK)
+
+
+def test_most_slots_and_long_rows():
+    """128 tokens of 64 slots on rows of 8192: the few-token kernels' LDS would not hold them."""
+    mx_case(small_inputs(128, 8192, 32, 256, 64, "bf16", "swiglu", "concat", seed=1))
+
+
+@pytest.mark.parametrize("T", [20, 150])
+def test_non_finite_tokens_stay_alone(T):
+    H, I, E = 160, 96, 5
+    ids = np.stack((np.arange(T) % E, (np.arange(T) + 1) % E), axis=1).astype(np.int32)
+    inp = small_inputs(T, H, I, E, 2, "bf16", "swiglu", "concat", seed=T, ids=ids)
+    gu, dn = (moe.mx_quantize(torch.from_numpy(v).cuda()) for v in (inp.w_gate_up, inp.w_down))
+    x, w = torch.from_numpy(inp.hidden).cuda().bfloat16(), torch.from_numpy(inp.topk_weights).cuda()
+    i = torch.from_numpy(ids).cuda()
+    want, _ = moe.mx_fwd(x, i, w, gu, dn)
+    x[3], x[T - 1, 5], w[7, 1] = float("nan"), float("inf"), float("inf")
+    got, _ = moe.mx_fwd(x, i, w, gu, dn)
+    assert torch.all(torch.isnan(got[3])) and not torch.any(torch.isfinite(got[7])) and not torch.all(torch.isfinite(got[T - 1]))
+    rest = [t for t in range(T) if t not in (3, 7, T - 1)]
+    assert torch.equal(got[rest], want[rest])
+
+
 @pytest.mark.parametrize("T", [4, 200])
 def test_bad_ids_are_dropped_and_reported(T):
     E = 5
@@ -254,3 +285,73 @@ def test_quantise_route_and_decode_together():
     dg, dd = moe.mx_dequantize(*gu), moe.mx_dequantize(*dn)
     check_layer(host(moe.fwd_few(x[:100], ids[:100], w[:100], dg, dd, **kw)[0]), ref[:100], bound[:100])
     check_layer(host(moe.fwd(x, ids, w, dg, dd, **kw)[0]), ref, bound)
+
+
+def test_rows_past_the_output_stay():
+    """A call of T tokens into the first rows of longer buffers leaves the rest as it was."""
+    for T in (1, 5, 150):
+        inp = small_inputs(T, 96, 64, 4, 2, "bf16", "swiglu", "concat", seed=T)
+        gu, dn = (moe.mx_quantize(torch.from_numpy(v).cuda()) for v in (inp.w_gate_up, inp.w_down))
+        x = torch.from_numpy(inp.hidden).cuda().bfloat16()
+        ids, w = torch.from_numpy(inp.topk_ids).cuda(), torch.from_numpy(inp.topk_weights).cuda()
+        big = torch.full((T + 40, 96), 7.0, dtype=torch.bfloat16, device="cuda")
+        moe.mx_fwd(x, ids, w, gu, dn, out=big[:T])
+        assert torch.all(big[T:] == 7) and torch.equal(big[:T], moe.mx_fwd(x, ids, w, gu, dn)[0])
+
+
+def test_quantize_into_the_callers_buffers():
+    w = torch.randn(6, 160, generator=torch.Generator().manual_seed(3)).cuda()
+    codes, scales = moe.mx_quantize(w)
+    pc = torch.full((10, 80), 0xEE, dtype=torch.uint8, device="cuda")
+    ps = torch.full((10, 5), 0xEE, dtype=torch.uint8, device="cuda")
+    moe.mx_quantize(w, out=(pc[:6], ps[:6]))
+    assert torch.equal(pc[:6], codes) and torch.equal(ps[:6], scales)
+    assert torch.all(pc[6:] == 0xEE) and torch.all(ps[6:] == 0xEE)
+    v = torch.full((8, 160), 7.0, device="cuda")
+    moe.mx_dequantize(codes, scales, dtype="fp32", out=v[:6])
+    assert torch.equal(v[:6], moe.mx_dequantize(codes, scales, dtype="fp32")) and torch.all(v[6:] == 7)
+
+
+def test_refusals_of_the_binding():
+    w = torch.randn(4, 96, device="cuda")
+    for bad in (w.t(), w[:, :48].contiguous(), w.half(), w[:, 0:0]):
+        with pytest.raises(ValueError):
+            moe.mx_quantize(bad)
+    with pytest.raises(moe.MoeError):
+        moe.mx_quantize(torch.randn(4 * 96 + 1, device="cuda")[1:].reshape(4, 96))   # not 16-byte aligned
+    codes, scales = moe.mx_quantize(w)
+    for c, s in ((codes, scales[:, :2]), (codes[:, :8], scales), (codes.int(), scales), (codes, scales.cpu())):
+        with pytest.raises(ValueError):
+            moe.mx_dequantize(c, s)
+    with pytest.raises(ValueError):
+        moe.mx_dequantize(codes, scales, dtype="fp16")
+    inp = small_inputs(4, 64, 32, 4, 2, "bf16", "swiglu", "concat")
+    gu, dn = (moe.mx_quantize(torch.from_numpy(v).cuda()) for v in (inp.w_gate_up, inp.w_down))
+    x = torch.from_numpy(inp.hidden).cuda().bfloat16()
+    ids, wt = torch.from_numpy(inp.topk_ids).cuda(), torch.from_numpy(inp.topk_weights).cuda()
+    for bad in [(x.float(), ids, wt, gu, dn), (x, ids, wt, dn, gu), (x, ids, wt, (gu[0], dn[1]), dn), (x, ids[:1], wt, gu, dn),
+                (x, ids, wt, (gu[0].to(torch.int8), gu[1]), dn)]:
+        with pytest.raises(ValueError):
+            moe.mx_fwd(*bad)
+    with pytest.raises(moe.MoeError) as e:
+        moe.mx_fwd(x, ids, wt, gu, dn, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == moe.MOE_ERR_WORKSPACE
+
+
+def test_two_streams_at_once():
+    """A prompt and a decode step on two streams, on the same weights."""
+    inps = [small_inputs(T, 256, 160, 8, 2, "bf16", "swiglu", "concat", seed=1) for T in (2, 300)]
+    gu, dn = (moe.mx_quantize(torch.from_numpy(v).cuda()) for v in (inps[0].w_gate_up, inps[0].w_down))
+    args = [(torch.from_numpy(i.hidden).cuda().bfloat16(), torch.from_numpy(i.topk_ids).cuda(),
+             torch.from_numpy(i.topk_weights).cuda(), gu, dn) for i in inps]
+    want = [moe.mx_fwd(*a)[0] for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(moe.mx_fwd(*args[i])[0])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
