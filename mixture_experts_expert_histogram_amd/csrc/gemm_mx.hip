@@ -6,13 +6,18 @@
 // rows of one expert on v_mfma_f32_16x16x32_bf16, BM x 64 a wave, fp32
 // accumulators.
 //
-// * The weights go from global memory straight to registers as codes, a whole
-//   cache line (256 k) of each of a wave's 64 rows at a time and one such line
-//   ahead.  A load covers 16 rows x 64 bytes: lane group g = lane / 16 holds
-//   block g of its row's 4 (32 x 32 tiles would take 32 rows x 32 bytes a
-//   load, which cost the loads' path twice the cache lines).  Each 8 codes
-//   become a bf16 fragment by four conversions that apply the scale (exact).
-//   No two waves share weight rows, so LDS would only add a copy.
+// * The weights go from global memory straight to registers as codes, one or
+//   two cache lines (256 or 512 k, a "line" below) of each of a wave's 64 rows
+//   at a time and one such line ahead.  A load covers 16 rows x 64 bytes: lane
+//   group g = lane / 16 holds block g of its row's 4 (32 x 32 tiles would take
+//   32 rows x 32 bytes a load, which cost the loads' path twice the cache
+//   lines).  Each 8 codes become a bf16 fragment by four conversions that apply
+//   the scale (exact).  No two waves share weight rows, so LDS would only add a
+//   copy.  Rows that do not start on a cache line (H = 2880: 1440 bytes) share
+//   their end lines between successive loads, and a tile's lines are evicted
+//   from L2 before the next load comes: 1.5 times the weights' bytes at 256 k,
+//   1.27 at 512, which the 32-position tiles have the registers for (512
+//   tokens 442 -> 430 us).
 // * The scales of the tile's rows go to LDS before the loop, in whole runs of
 //   rows: loaded from global memory a lane a block, they touch as many cache
 //   lines as the codes do.
@@ -23,7 +28,7 @@
 //   its end are loads past their buffer's end, which give zeros.
 // * A tile's 16-row blocks without a position are skipped (the count is the
 //   same for all waves), so a tile of few rows costs few products.
-// * Two or more workgroups a CU cover each other's waits.
+// * Two workgroups a CU cover each other's waits.
 #include <atomic>
 #include <type_traits>
 
@@ -45,7 +50,8 @@ struct MxCfg {
   static constexpr int FM = BM / 16, FN = 4;   // 16 x 16 blocks of a wave: positions, weight rows
   static constexpr int HALF = BM * 64;     // elements of a stage's 64-k half
   static constexpr int NB = BM / 8 / NW;   // 1 KB loads of a wave per half (8 rows of 128 bytes)
-  static constexpr int OCC = BM == 32 ? 3 : 2;   // waves a SIMD that the registers allow for
+  static constexpr int LS = BM == 32 ? 4 : 2;   // stages whose codes of a row are loaded together
+  static constexpr int OCC = 2;   // waves a SIMD that the registers allow for
 };
 
 // A raw buffer of 2^31 bytes at p (wave-uniform) as its four descriptor words.
@@ -109,19 +115,20 @@ struct WRows {
   __amdgpu_buffer_rsrc_t w[2];
   uint32_t off[4], sc[4];
 };
-// A cache line of each row: c[f][j] is the lane's block 4 j + g of the line's 8.
+// LS stages' codes of each row: c[f][j] is the lane's block 4 j + g of them.
+template <int LS>
 struct WLine {
-  u32x4_t c[4][2];
+  u32x4_t c[4][LS];
 };
-// Groups 2 h and 2 h + 1 of line t.
-template <bool GATE_UP>
-__device__ __forceinline__ void load_line(const WRows& r, int h, int t, int nb, int lane, WLine& w) {
+// Part J of line t: 4 / LS of the groups.
+template <bool GATE_UP, int LS>
+__device__ __forceinline__ void load_line(const WRows& r, int part, int t, int nb, int lane, WLine<LS>& w) {
 #pragma unroll
-  for (int f = 2 * h; f < 2 * h + 2; ++f)
+  for (int f = 4 / LS * part; f < 4 / LS * (part + 1); ++f)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int b = t * 8 + 4 * j + (lane >> 4);
-      w.c[f][j] = load16(r.w[GATE_UP ? h : 0], b < nb ? r.off[f] + b * 16 : kPast);
+    for (int j = 0; j < LS; ++j) {
+      const int b = t * 4 * LS + 4 * j + (lane >> 4);
+      w.c[f][j] = load16(r.w[GATE_UP ? f >> 1 : 0], b < nb ? r.off[f] + b * 16 : kPast);
     }
 }
 
@@ -147,7 +154,7 @@ __device__ __forceinline__ void read_scales(const uint8_t* scales, const WRows& 
 // stage's scale bytes and, afterwards, the next stage's.
 template <class C, int NF, class Issue>
 __device__ __forceinline__ void stage_products(const uint16_t* stage, const uint8_t* scales, const WRows& r,
-                                               const WLine& w, int j, int s, int nb, uint32_t (&sb)[4],
+                                               const WLine<C::LS>& w, int j, int s, int nb, uint32_t (&sb)[4],
                                                f32x4 (&acc)[C::FM][C::FN], int lane, Issue issue) {
   const int r16 = lane & 15, g = lane >> 4;
   const uint16_t* half = stage + (g >> 1) * C::HALF;
@@ -183,23 +190,23 @@ __device__ __forceinline__ void stage_products(const uint16_t* stage, const uint
 
 constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }   // vmcnt <= n, lgkmcnt 0
 
-// Stage s = 2 t + J: the stage's activations have landed (they were issued one
+// Stage s = LS t + J: the stage's activations have landed (they were issued one
 // stage ago, before that stage's 4 weight loads: of those the first stage of a
-// line needs the last ones itself, the second leaves them in flight; at the
+// line needs the last ones itself, the others leave them in flight; at the
 // loop's end, where some have no use and are not issued, nothing is counted on)
 // and every wave is past its reads of the stage before, whose buffer the next
 // stage's loads then fill (zeros, past the last stage).
 template <class C, bool GATE_UP, int NF, int J, bool TAIL = false>
 __device__ __forceinline__ void one_stage(const ActRows<C>& ar, const WRows& wr, const uint8_t* scales, int t, int nb,
-                                          int K, uint16_t* lds, const WLine& cur, WLine& next,
+                                          int K, uint16_t* lds, const WLine<C::LS>& cur, WLine<C::LS>& next,
                                           uint32_t (&sb)[4], f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
-  const int s = 2 * t + J;
+  const int s = C::LS * t + J;
   __builtin_amdgcn_s_waitcnt(wait_vm(J == 0 || TAIL ? 0 : 4));
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  stage_products<C, NF>(lds + J * 2 * C::HALF, scales, wr, cur, J, s, nb, sb, acc, lane, [&] {
-    ar.issue(s + 1, K, lds + (J ^ 1) * 2 * C::HALF, wave);
+  stage_products<C, NF>(lds + (J & 1) * 2 * C::HALF, scales, wr, cur, J, s, nb, sb, acc, lane, [&] {
+    ar.issue(s + 1, K, lds + (~J & 1) * 2 * C::HALF, wave);
     load_line<GATE_UP>(wr, J, t + 1, nb, lane, next);
     asm volatile("" ::: "memory");   // the loads stay here: the next stage's wait counts them
     __builtin_amdgcn_sched_barrier(0);
@@ -212,29 +219,59 @@ __device__ __forceinline__ void one_stage(const ActRows<C>& ar, const WRows& wr,
 // the activations just issued among it.
 template <class C, bool GATE_UP, int NF>
 __device__ __forceinline__ void mainloop(const ActRows<C>& ar, const WRows& wr, const uint8_t* scales, int K, uint16_t* lds,
-                                         WLine& l0, f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
+                                         WLine<C::LS>& l0, f32x4 (&acc)[C::FM][C::FN], int wave, int lane) {
   const int nb = K >> 5, ns = (nb + 3) >> 2;
-  WLine l1;
+  WLine<C::LS> l1;
   uint32_t sb[4];
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();   // every wave's scales are in LDS
   asm volatile("" ::: "memory");
   read_scales(scales, wr, 0, nb, lane, sb);
+  const auto stage = [&](auto j, auto tail, int t, const WLine<C::LS>& cur, WLine<C::LS>& next) {
+    one_stage<C, GATE_UP, NF, decltype(j)::value, decltype(tail)::value>(ar, wr, scales, t, nb, K, lds, cur, next, sb, acc, wave,
+                                                                          lane);
+  };
+  using std::integral_constant;
+  using no = std::false_type;
+  using yes = std::true_type;
   int t = 0;
-  for (; 2 * t + 4 <= ns; t += 2) {
-    one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
-    one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
-    one_stage<C, GATE_UP, NF, 0>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, sb, acc, wave, lane);
-    one_stage<C, GATE_UP, NF, 1>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, sb, acc, wave, lane);
-  }
-  if (2 * t < ns) {
-    one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
-    if (2 * t + 1 < ns) {
-      one_stage<C, GATE_UP, NF, 1, true>(ar, wr, scales, t, nb, K, lds, l0, l1, sb, acc, wave, lane);
-      if (2 * t + 2 < ns) one_stage<C, GATE_UP, NF, 0, true>(ar, wr, scales, t + 1, nb, K, lds, l1, l0, sb, acc, wave, lane);
+  for (; C::LS * (t + 2) <= ns; t += 2) {
+    stage(integral_constant<int, 0>{}, no{}, t, l0, l1);
+    stage(integral_constant<int, 1>{}, no{}, t, l0, l1);
+    if constexpr (C::LS == 4) {
+      stage(integral_constant<int, 2>{}, no{}, t, l0, l1);
+      stage(integral_constant<int, 3>{}, no{}, t, l0, l1);
+    }
+    stage(integral_constant<int, 0>{}, no{}, t + 1, l1, l0);
+    stage(integral_constant<int, 1>{}, no{}, t + 1, l1, l0);
+    if constexpr (C::LS == 4) {
+      stage(integral_constant<int, 2>{}, no{}, t + 1, l1, l0);
+      stage(integral_constant<int, 3>{}, no{}, t + 1, l1, l0);
     }
   }
+  // what is left: less than two lines, each stage behind the question whether it exists
+  const int left = ns - C::LS * t;
+  [&] {
+    if (left < 1) return;
+    stage(integral_constant<int, 0>{}, yes{}, t, l0, l1);
+    if (left < 2) return;
+    stage(integral_constant<int, 1>{}, yes{}, t, l0, l1);
+    if constexpr (C::LS == 4) {
+      if (left < 3) return;
+      stage(integral_constant<int, 2>{}, yes{}, t, l0, l1);
+      if (left < 4) return;
+      stage(integral_constant<int, 3>{}, yes{}, t, l0, l1);
+    }
+    if (left <= C::LS) return;
+    stage(integral_constant<int, 0>{}, yes{}, t + 1, l1, l0);
+    if constexpr (C::LS == 4) {
+      if (left < 6) return;
+      stage(integral_constant<int, 1>{}, yes{}, t + 1, l1, l0);
+      if (left < 7) return;
+      stage(integral_constant<int, 2>{}, yes{}, t + 1, l1, l0);
+    }
+  }();
   __builtin_amdgcn_s_waitcnt(wait_vm(0));   // no load into LDS outlives the tile
 }
 
@@ -271,7 +308,7 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx_gemm_kernel(MxArgs p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int K = GATE_UP ? g.H : g.I, nb = K >> 5;
   WRows wr;
-  WLine l0;
+  WLine<C::LS> l0;
   // the tile's first column, its columns, and the wave's own
   constexpr int BC = GATE_UP ? C::BN / 2 : C::BN, WC = BC / C::NW;
   const int c0 = nt * BC, ncol = min(BC, (GATE_UP ? g.I : g.H) - c0);
@@ -286,8 +323,8 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx_gemm_kernel(MxArgs p) {
     wr.off[f] = rs * (uint32_t)j;
     wr.sc[f] = nb * (GATE_UP ? (inter ? 2 * j + (f >> 1) : (f >> 1) * ncol + j) : j);
   }
-  load_line<GATE_UP>(wr, 0, 0, nb, lane, l0);
-  load_line<GATE_UP>(wr, 1, 0, nb, lane, l0);
+#pragma unroll
+  for (int part = 0; part < C::LS; ++part) load_line<GATE_UP>(wr, part, 0, nb, lane, l0);
   ActRows<C> ar;
   ar.rs = buffer_words(GATE_UP ? g.A : (const void*)((const uint16_t*)g.A + (size_t)m0 * g.I));
 #pragma unroll
@@ -388,9 +425,9 @@ hipError_t launch(const GemmProblem& pb, MxArgs p, const char* name, hipStream_t
 }
 
 // Tiles of 32 positions for experts of at most 16 on average, where reading
-// the weights is all of the time (more workgroups a CU: gpt-oss-shaped layer at
-// 256 tokens, 8 an expert, 402 us against 413; at 512 both 442), else of 64
-// (1024 tokens 503 us against 516, 4096 tokens 1.00 ms against 1.14).  Tiles of
+// the weights is all of the time (gpt-oss-shaped layer at 256 tokens, 8 an
+// expert, 392 us against 413; 512 tokens 430 against 442), else of 64 (1024
+// tokens 503 us against 516, 4096 tokens 0.98 ms against 1.14).  Tiles of
 // 128 positions x 512 rows on 8 waves move a third less through the load path,
 // but one workgroup a CU leaves its waits and its ends uncovered: 1.01 ms at
 // 4096 tokens, 3.32 against 3.37 ms at 16384.
