@@ -461,13 +461,20 @@ moe_status_t few_check(const Dims& d) {
 }
 
 // Large layers whose experts hold more than 32 slots on average: the few-token
-// kernels, which read 32 tokens' rows for every 32 to 64 weight rows, are then
-// bound by those and take the weights in several passes, and the routed
-// products are faster (H = I = 2880, 8 experts, top-4, 128 tokens: bf16 137 us
-// against 240, 4-bit 83 against 103; 64 tokens 128 against 146 and 70 against
-// 70).  Small layers stay: their time is launches (1024 x 1024, 4 experts,
-// top-2, 64 tokens: 23 us against 59).
-bool many_slots(const Dims& d) { return d.S > 32 * d.E && d.H * d.I >= (int64_t(1) << 21); }
+// kernels, which read 32 to 64 tokens' rows for every 32 to 64 weight rows, are
+// then bound by those and take the weights in several passes, and the routed
+// products are faster (us, few-token kernels against routed products):
+//   experts of H x I, tokens, top-k    slots/E   bf16        4-bit
+//    8 of 2880 x 2880, 128, 4               64   215  138    122   93
+//    8 of 2880 x 2880,  64, 4               32   132  132     75   81
+//   10 of 4096 x 2880, 128, 4               51   273  184    159  101
+//   16 of 2880 x 1440, 128, 8               64   205  129    115   94
+//    8 of 4096 x 2048, 128, 2               32   119  141     66   82
+// Small layers stay, where the routing is the larger part:
+//    8 of 2048 x 1024,  64, 8               64    53   83
+//    4 of 2048 x 2048, 128, 4              128    87   96
+//    4 of 2048 x 1024, 128, 4              128    54   82     61   56
+bool many_slots(const Dims& d) { return d.S > 32 * d.E && d.E * d.H * d.I > (int64_t(1) << 24); }
 
 // Microscaled 4-bit weights: whole blocks of 32 columns, bf16 activations.
 moe_status_t mx_check(const Dims& d) {

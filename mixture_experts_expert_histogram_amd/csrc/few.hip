@@ -246,15 +246,15 @@ __device__ __forceinline__ int find_slots(const FewArgs& p, int e, uint16_t* lis
   return c;
 }
 
-// The waves' partial sums in LDS: [wave][group][column tile][column 16][row
-// 16], read back summed in wave order.
-template <int G, int NT>
-__device__ __forceinline__ void put_partial(float* red, int wave, int lane, const f32x4 (&acc)[G][NT]) {
+// The waves' partial sums of RT column tiles from n0 in LDS: [wave][group]
+// [column tile][column 16][row 16], read back summed in wave order.
+template <int G, int NT, int RT>
+__device__ __forceinline__ void put_partial(float* red, int wave, int lane, const f32x4 (&acc)[G][NT], int n0) {
 #pragma unroll
   for (int h = 0; h < G; ++h)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      *(f32x4*)(red + (((wave * G + h) * NT + n) * 16 + (lane & 15)) * 16 + 4 * (lane >> 4)) = acc[h][n];
+    for (int n = 0; n < RT; ++n)
+      *(f32x4*)(red + (((wave * G + h) * RT + n) * 16 + (lane & 15)) * 16 + 4 * (lane >> 4)) = acc[h][n0 + n];
 }
 // element (row j, token column c) of group h
 template <int G, int NT, int NW>
@@ -268,13 +268,20 @@ __device__ __forceinline__ float get_sum(const float* red, int h, int j, int c) 
 template <int KIND> struct Elem { using T = uint16_t; };
 template <> struct Elem<W_F32> { using T = float; };
 
-// Per weight kind: row groups of a wave, units in flight, waves of a
-// workgroup, waves a SIMD that the registers allow for, and column tiles of an
-// expert with more than 16 tokens.
+// Per weight kind: row groups of a wave, units in flight with one column tile
+// and with more, waves of a workgroup, waves a SIMD that the registers allow
+// for, and the most column tiles of a pass.  Up to 64 tokens of an expert are
+// one pass over its weights: with passes of 32, 8 experts of 2880 x 2880 took
+// 156 us at 64 tokens, top-4, and take 132 (4-bit weights, whose fragments of
+// 64 rows leave no registers for it, stay at 32).  4 row groups for plain
+// weights read each token row half as often and were faster above 30 tokens an
+// expert (125 us there), but slower below (16 tokens, 128 experts: 484 us
+// against 428) and in small layers.
 template <int KIND> struct Tune;
-template <> struct Tune<W_BF16> { static constexpr int G = 2, D1 = 2, D2 = 1, NW = 4, OCC = 4, NT2 = 2; };
-template <> struct Tune<W_F32> { static constexpr int G = 2, D1 = 2, D2 = 1, NW = 4, OCC = 4, NT2 = 2; };
-template <> struct Tune<W_MX> { static constexpr int G = 4, D1 = 1, D2 = 1, NW = 4, OCC = 3, NT2 = 2; };
+template <> struct Tune<W_BF16> { static constexpr int G = 2, D1 = 2, D2 = 1, NW = 4, OCC = 4, NT = 4; };
+template <> struct Tune<W_F32> { static constexpr int G = 2, D1 = 2, D2 = 1, NW = 4, OCC = 4, NT = 4; };
+template <> struct Tune<W_MX> { static constexpr int G = 4, D1 = 1, D2 = 1, NW = 4, OCC = 3, NT = 2; };
+constexpr int RED_NT = 2;   // column tiles whose partial sums are in LDS at once
 
 // Rows of G/2 gate and up groups: groups 2i and 2i+1 are the gate and up rows
 // of activation columns j0 + 16 i .. +15.
@@ -343,17 +350,21 @@ __device__ __forceinline__ void gate_up_pass(const FewArgs& p, const Rows<G>& r,
   f32x4 acc[G][NT];
   zero<G, NT>(acc);
   dot.run(r, rsrc(p.X), xoff, wave, NW, p.H, lane, acc);
-  put_partial<G, NT>(red, wave, lane, acc);
-  lds_sync();
   T* a = (T*)p.a;
-  for (int o = threadIdx.x; o < 8 * G * 16 * NT; o += NW * 64) {
-    const int j = o % (8 * G), t = o / (8 * G);
-    if (c0 + t < c && j0 + j < p.I) {
-      const float gv = get_sum<G, NT, NW>(red, 2 * (j >> 4), j & 15, t), uv = get_sum<G, NT, NW>(red, 2 * (j >> 4) + 1, j & 15, t);
-      store_val<T>(a + (size_t)list[c0 + t] * p.I + j0 + j, glu_fwd(gv, uv, p.act, p.limit, p.alpha));
+  constexpr int RT = NT < RED_NT ? NT : RED_NT;
+#pragma unroll
+  for (int n0 = 0; n0 < NT; n0 += RT) {
+    put_partial<G, NT, RT>(red, wave, lane, acc, n0);
+    lds_sync();
+    for (int o = threadIdx.x; o < 8 * G * 16 * RT; o += NW * 64) {
+      const int j = o % (8 * G), t = o / (8 * G), i = c0 + n0 * 16 + t;
+      if (i < c && j0 + j < p.I) {
+        const float gv = get_sum<G, RT, NW>(red, 2 * (j >> 4), j & 15, t), uv = get_sum<G, RT, NW>(red, 2 * (j >> 4) + 1, j & 15, t);
+        store_val<T>(a + (size_t)list[i] * p.I + j0 + j, glu_fwd(gv, uv, p.act, p.limit, p.alpha));
+      }
     }
+    lds_sync();
   }
-  lds_sync();
 }
 
 template <int KIND>
@@ -362,7 +373,7 @@ __global__ __launch_bounds__(Tune<KIND>::NW * 64, Tune<KIND>::OCC) void few_gate
   constexpr int G = TU::G, NW = TU::NW;
   extern __shared__ char few_lds[];
   __shared__ int cnt[NW];
-  __shared__ __align__(16) float red[NW * G * TU::NT2 * 256];
+  __shared__ __align__(16) float red[NW * G * RED_NT * 256];
   uint16_t* list = (uint16_t*)few_lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (blockIdx.x == 0 && blockIdx.y == 0 && wave == 0) {   // slots with an id outside [0,E)
@@ -395,11 +406,16 @@ __global__ __launch_bounds__(Tune<KIND>::NW * 64, Tune<KIND>::OCC) void few_gate
       scales.store(sc, threadIdx.x);
       lds_sync();
     }
-    for (int c0 = 0; c0 < c; c0 += 16 * TU::NT2) {
-      Dot<KIND, G, TU::NT2, TU::D2> dot2;
-      dot2.start(r, wave, NW, p.H, lane);
-      gate_up_pass<KIND, G, TU::NT2, TU::D2, NW>(p, r, dot2, j0, c0, c, list, red, wave, lane);
-    }
+    const auto pass = [&](auto n, int c0) {
+      constexpr int NT = decltype(n)::value;
+      Dot<KIND, G, NT, TU::D2> dot;
+      dot.start(r, wave, NW, p.H, lane);
+      gate_up_pass<KIND, G, NT, TU::D2, NW>(p, r, dot, j0, c0, c, list, red, wave, lane);
+    };
+    int c0 = 0;
+    if constexpr (TU::NT > 2)
+      for (; c - c0 > 32; c0 += 16 * TU::NT) pass(std::integral_constant<int, TU::NT>{}, c0);
+    for (; c0 < c; c0 += 32) pass(std::integral_constant<int, 2>{}, c0);
   }
 }
 
@@ -417,16 +433,20 @@ __device__ __forceinline__ void down_pass(const FewArgs& p, const Rows<G>& r, Do
   f32x4 acc[G][NT];
   zero<G, NT>(acc);
   dot.run(r, rsrc(p.a), xoff, wave, NW, p.I, lane, acc);
-  put_partial<G, NT>(red, wave, lane, acc);
-  lds_sync();
-  for (int o = threadIdx.x; o < 16 * G * 16 * NT; o += NW * 64) {
-    const int j = o % (16 * G), t = o / (16 * G);
-    if (c0 + t < c && h0 + j < p.H) {
-      const int s = list[c0 + t];
-      p.y[(size_t)s * p.H + h0 + j] = p.w[s] * get_sum<G, NT, NW>(red, j >> 4, j & 15, t);
+  constexpr int RT = NT < RED_NT ? NT : RED_NT;
+#pragma unroll
+  for (int n0 = 0; n0 < NT; n0 += RT) {
+    put_partial<G, NT, RT>(red, wave, lane, acc, n0);
+    lds_sync();
+    for (int o = threadIdx.x; o < 16 * G * 16 * RT; o += NW * 64) {
+      const int j = o % (16 * G), t = o / (16 * G), i = c0 + n0 * 16 + t;
+      if (i < c && h0 + j < p.H) {
+        const int s = list[i];
+        p.y[(size_t)s * p.H + h0 + j] = p.w[s] * get_sum<G, RT, NW>(red, j >> 4, j & 15, t);
+      }
     }
+    lds_sync();
   }
-  lds_sync();
 }
 
 template <int KIND>
@@ -435,7 +455,7 @@ __global__ __launch_bounds__(Tune<KIND>::NW * 64, Tune<KIND>::OCC) void few_down
   constexpr int G = TU::G, NW = TU::NW;
   extern __shared__ char few_lds[];
   __shared__ int cnt[NW];
-  __shared__ __align__(16) float red[NW * G * TU::NT2 * 256];
+  __shared__ __align__(16) float red[NW * G * RED_NT * 256];
   uint16_t* list = (uint16_t*)few_lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e = expert_of(p);
@@ -461,11 +481,16 @@ __global__ __launch_bounds__(Tune<KIND>::NW * 64, Tune<KIND>::OCC) void few_down
       scales.store(sc, threadIdx.x);
       lds_sync();
     }
-    for (int c0 = 0; c0 < c; c0 += 16 * TU::NT2) {
-      Dot<KIND, G, TU::NT2, TU::D2> dot2;
-      dot2.start(r, wave, NW, p.I, lane);
-      down_pass<KIND, G, TU::NT2, TU::D2, NW>(p, r, dot2, h0, c0, c, list, red, wave, lane);
-    }
+    const auto pass = [&](auto n, int c0) {
+      constexpr int NT = decltype(n)::value;
+      Dot<KIND, G, NT, TU::D2> dot;
+      dot.start(r, wave, NW, p.I, lane);
+      down_pass<KIND, G, NT, TU::D2, NW>(p, r, dot, h0, c0, c, list, red, wave, lane);
+    };
+    int c0 = 0;
+    if constexpr (TU::NT > 2)
+      for (; c - c0 > 32; c0 += 16 * TU::NT) pass(std::integral_constant<int, TU::NT>{}, c0);
+    for (; c0 < c; c0 += 32) pass(std::integral_constant<int, 2>{}, c0);
   }
 }
 

@@ -88,7 +88,7 @@ def test_one_token_from_logits(E):
             assert torch.equal(out, moe.fwd_few(d["hidden"], ids, w, d["w_gate_up"], d["w_down"])[0])
 
 
-@pytest.mark.parametrize("T", [16, 17, 32, 33, 65, 128])
+@pytest.mark.parametrize("T", [16, 17, 32, 33, 48, 64, 65, 96, 97, 128])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_one_expert_takes_every_token(T, dtype):
     ids = np.full((T, 1), 2, dtype=np.int32)
@@ -98,8 +98,13 @@ def test_one_expert_takes_every_token(T, dtype):
 
 @pytest.mark.parametrize("T", [32, 33, 128])
 def test_large_layer_of_few_experts(T):
-    """Sizes on both sides of the rule that hands a call to the forward's kernels (32 slots an expert, H I of 2^21)."""
     run_case(small_inputs(T, 1456, 1456, 2, 2, "bf16", "clamped", "interleaved", seed=T))
+
+
+@pytest.mark.parametrize("T", [32, 33, 100])
+def test_sides_of_the_rule_of_many_slots(T):
+    """32 slots an expert and more in a layer of E H I over 2^24: the latter run the forward's kernels."""
+    run_case(small_inputs(T, 1456, 1456, 8, 8, "bf16", "clamped", "concat", seed=T))
 
 
 def test_repeated_ids_of_one_token():

@@ -144,8 +144,13 @@ def test_one_expert_takes_every_token(T):
 
 @pytest.mark.parametrize("T", [32, 33, 128])
 def test_large_layer_of_few_experts(T):
-    """Sizes on both sides of the rule between the few-token kernels and the grouped products."""
     mx_case(small_inputs(T, 1472, 1472, 2, 2, "bf16", "swiglu", "concat", seed=T))
+
+
+@pytest.mark.parametrize("T", [32, 33, 100])
+def test_sides_of_the_rule_of_many_slots(T):
+    """32 slots an expert and more in a layer of E H I over 2^24: the latter run the grouped products."""
+    mx_case(small_inputs(T, 1472, 1472, 8, 8, "bf16", "clamped", "interleaved", seed=T))
 
 
 @pytest.mark.parametrize("T", [3, 140])
