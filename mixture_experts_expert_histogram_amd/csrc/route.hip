@@ -39,26 +39,61 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_hist_kernel(
   if (threadIdx.x == 0) blk_bad[blockIdx.x] = bad;
 }
 
-// Exclusive scan over one value per thread of a 1024-thread block, by shuffles
-// inside each wavefront and the 16 wavefronts' totals in LDS (two barriers a
-// scan instead of 22: the routing scan makes nine of them, which took most of
-// its time).  sh[1023] holds the block's total until the next scan.
-__device__ int block_exclusive_scan_1024(int v, int* sh) {
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  int incl = v;
+// Inclusive scan over a wavefront's lanes, in registers: rows of 16 lanes,
+// then the rows' totals.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_inclusive_scan(int v) {
+  v = dpp_add<0x111, 0xF>(v);   // row_shr 1, 2, 4, 8
+  v = dpp_add<0x112, 0xF>(v);
+  v = dpp_add<0x114, 0xF>(v);
+  v = dpp_add<0x118, 0xF>(v);
+  v = dpp_add<0x142, 0xA>(v);   // lane 15 of a row to the next, into rows 1 and 3
+  return dpp_add<0x143, 0xC>(v);   // lane 31 into rows 2 and 3
+}
+
+// Exclusive scans over N values per thread of a 1024-thread block, in place:
+// in registers inside each wavefront, the wavefronts' totals through LDS, two
+// barriers for all of them (by shuffles through LDS, all wavefronts, they took
+// 6 us of the routing).  Only the first `nw` wavefronts have values other
+// than zero, and only theirs are returned.  sh keeps the totals until the next
+// call.
+template <int N>
+__device__ __forceinline__ void block_exclusive_scans_1024(int (&v)[N], int (&sh)[N][16], int nw) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int incl[N];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(incl, d);
-    if (lane >= d) incl += o;
+  for (int j = 0; j < N; ++j) {
+    incl[j] = wave < nw ? wave_inclusive_scan(v[j]) : 0;
+    if (lane == 63) sh[j][wave] = incl[j];
   }
-  if (lane == 63) sh[wave] = incl;
   __syncthreads();
-  int base = 0;
+  if (wave < nw) {
+    int base[N] = {};
+    for (int w = 0; w < wave; ++w)
 #pragma unroll
-  for (int w = 0; w < 16; ++w) base += w < wave ? sh[w] : 0;
-  if (t == 1023) sh[1023] = base + incl;
+      for (int j = 0; j < N; ++j) base[j] += sh[j][w];
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = base[j] + incl[j] - v[j];
+  }
   __syncthreads();
-  return base + incl - v;
+}
+// The total of scan j (all threads, until the next call writes sh).
+template <int N>
+__device__ __forceinline__ int scan_total(const int (&sh)[N][16], int j) {
+  int n = 0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) n += sh[j][w];
+  return n;
+}
+
+// Tiles of an expert of c slots in table j.
+__device__ __forceinline__ int tiles_of(int j, int c, int big_min, int small_bm) {
+  const int bm = tile_bm(j), set = tile_set(j);
+  const bool in = set == 0 || (set == 1) == large_tile_expert(c, big_min, small_bm);
+  return in ? (c + bm - 1) / bm : 0;
 }
 
 // Pass 2 (one workgroup): counts, offsets, per-chunk bases, M-tile tables,
@@ -71,7 +106,8 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(int nblk, int E, int b
                                                           int32_t* __restrict__ tile_prefix,
                                                           int32_t* __restrict__ expert_order,
                                                           int32_t* __restrict__ status) {
-  __shared__ int sh[1024];
+  __shared__ int sh[1][16];
+  __shared__ int sht[N_TILE_TABLES][16];
   __shared__ int cnt[MAX_E];
   __shared__ int part[1024];   // [slice][expert]: per-slice sums, then their bases
   __shared__ int base[MAX_E];
@@ -89,15 +125,13 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(int nblk, int E, int b
   constexpr int U = 16;
   if (slice_thread) {
     int sum = 0;
-    int b = b0;
-    for (; b + U <= b1; b += U) {
+    for (int b = b0; b < b1; b += U) {
       int v[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = blk_hist[(size_t)(b + u) * E + te];
+      for (int u = 0; u < U; ++u) v[u] = b + u < b1 ? blk_hist[(size_t)(b + u) * E + te] : 0;
 #pragma unroll
       for (int u = 0; u < U; ++u) sum += v[u];
     }
-    for (; b < b1; ++b) sum += blk_hist[(size_t)b * E + te];
     part[threadIdx.x] = sum;
   }
   __syncthreads();
@@ -108,7 +142,9 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(int nblk, int E, int b
       part[q * E + e] = c;
       c += v;
     }
-  const int off = block_exclusive_scan_1024(c, sh);
+  int one[1] = {c};
+  block_exclusive_scans_1024<1>(one, sh, (E + 63) / 64);
+  const int off = one[0];
   if (e < E) {
     counts[e] = c;
     offsets[e] = off;
@@ -119,38 +155,30 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(int nblk, int E, int b
   __syncthreads();
   if (slice_thread) {   // per-chunk bases of the expert's slots, chunk by chunk
     int run = base[te] + part[threadIdx.x];
-    int b = b0;
-    for (; b + U <= b1; b += U) {
+    for (int b = b0; b < b1; b += U) {
       int h[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) h[u] = blk_hist[(size_t)(b + u) * E + te];
+      for (int u = 0; u < U; ++u) h[u] = b + u < b1 ? blk_hist[(size_t)(b + u) * E + te] : 0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        blk_hist[(size_t)(b + u) * E + te] = run;
+        if (b + u < b1) blk_hist[(size_t)(b + u) * E + te] = run;
         run += h[u];
       }
     }
-    for (; b < b1; ++b) {
-      const int h = blk_hist[(size_t)b * E + te];
-      blk_hist[(size_t)b * E + te] = run;
-      run += h;
-    }
   }
+  int nt[N_TILE_TABLES], tp[N_TILE_TABLES];
+#pragma unroll
+  for (int j = 0; j < N_TILE_TABLES; ++j) nt[j] = tp[j] = e < E ? tiles_of(j, c, big_min, small_bm) : 0;
+  block_exclusive_scans_1024<N_TILE_TABLES>(tp, sht, (E + 63) / 64);
+#pragma unroll
   for (int j = 0; j < N_TILE_TABLES; ++j) {
-    const int bm = tile_bm(j), set = tile_set(j);
-    const bool in = set == 0 || (set == 1) == large_tile_expert(c, big_min, small_bm);
-    const int nt = (e < E && in) ? (c + bm - 1) / bm : 0;
-    const int p = block_exclusive_scan_1024(nt, sh);
-    if (e < E) tile_prefix[j * (E + 1) + e] = p;
-    if (e == E - 1) tile_prefix[j * (E + 1) + E] = p + nt;
+    if (e < E) tile_prefix[j * (E + 1) + e] = tp[j];
+    if (e == E - 1) tile_prefix[j * (E + 1) + E] = tp[j] + nt[j];
   }
-  __syncthreads();
   if (e < E) {
-    int r = 0;
-    for (int e2 = 0; e2 < E; ++e2) {
-      const int c2 = cnt[e2];
-      r += (c2 > c) || (c2 == c && e2 < e);
-    }
+    int r = 0;   // experts of more slots, and of as many with a lower id
+#pragma unroll 8
+    for (int e2 = 0; e2 < E; ++e2) r += cnt[e2] > (e2 < e ? c - 1 : c);
     expert_order[r] = e;
   }
   // Slots with an id outside [0,E) go after every valid slot, chunk by chunk
@@ -162,13 +190,26 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(int nblk, int E, int b
   for (int c0 = 0; c0 < nblk; c0 += 1024) {
     const int b = c0 + threadIdx.x;
     const int h = b < nblk ? blk_bad[b] : 0;
-    const int ex = block_exclusive_scan_1024(h, sh);
-    const int tot = sh[1023];   // inclusive total of this group of chunks
-    __syncthreads();            // read before the next group's scan writes sh
-    if (b < nblk) blk_bad[b] = run + ex;
+    int ex[1] = {h};
+    block_exclusive_scans_1024<1>(ex, sh, 16);
+    const int tot = scan_total(sh, 0);   // of this group of chunks
+    __syncthreads();                     // read before the next group's scan writes sh
+    if (b < nblk) blk_bad[b] = run + ex[0];
     run += tot;
   }
   if (threadIdx.x == 0) status[0] = run - valid;
+}
+
+// The lanes of the wave that hold this lane's key (at least 0, `bits` bits; a
+// lane with a negative key is in nobody's set): one ballot per bit.
+__device__ __forceinline__ uint64_t same_key(int key, int bits) {
+  uint64_t peers = __ballot(key >= 0);
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (key >> b) & 1;
+    const uint64_t m = __ballot(one);
+    peers &= one ? m : ~m;
+  }
+  return peers;
 }
 
 // Pass 3: stable scatter.  A chunk is walked in rounds of 256 consecutive
@@ -195,6 +236,7 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_scatter_kernel(
   }
   __syncthreads();
   const uint64_t lower = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
+  const int bits = 32 - __clz(E);
   for (int r = 0; r < ROUTE_CHUNK / ROUTE_THREADS; ++r) {
     const int s = blockIdx.x * ROUTE_CHUNK + r * ROUTE_THREADS + tid;
     int e = -1;   // grouping key: the expert id, E for a bad id, -1 past the end
@@ -202,15 +244,7 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_scatter_kernel(
       e = ids[s];
       if ((unsigned)e >= (unsigned)E) e = E;
     }
-    uint64_t peers = 0;
-    uint64_t todo = __ballot(e >= 0);
-    while (todo) {                       // wave-uniform loop over distinct keys
-      const int leader = __ffsll((unsigned long long)todo) - 1;
-      const int le = __shfl(e, leader);
-      const uint64_t m = __ballot(e == le);
-      if (e == le) peers = m;
-      todo &= ~m;
-    }
+    const uint64_t peers = same_key(e, bits);
     const int rank = __popcll(peers & lower);
     if (e >= 0 && rank == 0) wcnt[wave][e] = __popcll(peers);
     __syncthreads();
@@ -234,6 +268,115 @@ __global__ __launch_bounds__(ROUTE_THREADS) void route_scatter_kernel(
       running[e2] += add;
     }
     __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// All three passes in one workgroup, for up to 1024 R slots, where launches
+// and trips through memory are most of the passes' time: 5.9 us at 2048 slots
+// of 128 experts (the three kernels took 28 in all), 12.0 at 8192, past which
+// the passes' 15 us and two launches are as fast.  Same outputs, bit for bit.
+//
+// Wave v takes the 64 R consecutive slots from 64 R v.  A slot's rank among
+// its wave's slots of the same key (expert, or E for a bad id) is the number
+// of lower lanes of the same key in its round, found with one ballot per bit of
+// the key, after the key's count in the wave's earlier rounds; the waves'
+// counts are then scanned in wave order.  The permutation is put in order in
+// LDS, so that positions are written in whole lines.
+constexpr int ROUTE_ONE_MAX = 8192;
+template <int R>
+__global__ __launch_bounds__(1024) void route_one_kernel(const int32_t* __restrict__ ids, const float* __restrict__ w, int S,
+                                                         int K, int E, RouteState rs) {
+  constexpr int N = 1 + N_TILE_TABLES;
+  __shared__ uint16_t wcnt[16][MAX_E + 2];   // by wave and key: count, then the count of the waves before
+  __shared__ uint16_t list[R * 1024];        // slot of a position
+  __shared__ __align__(16) int ord[MAX_E];
+  __shared__ int base[MAX_E + 1];            // first position of a key
+  __shared__ int sh[N][16];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const uint64_t lower = lane == 0 ? 0ull : ~0ull >> (64 - lane);
+  int key[R], rank[R];   // key: -1 past the end
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int s = (wave * R + r) * 64 + lane;
+    key[r] = -1;
+    if (s < S) {
+      const int e = ids[s];
+      key[r] = (unsigned)e < (unsigned)E ? e : E;
+    }
+  }
+  for (int e = lane; e <= E; e += 64) wcnt[wave][e] = 0;
+  asm volatile("" ::: "memory");   // a wave's LDS accesses run in order; the compiler keeps them so
+  const int bits = 32 - __clz(E);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int e = key[r];
+    const uint64_t peers = same_key(e, bits);
+    int before = 0;
+    if (e >= 0) before = wcnt[wave][e];
+    asm volatile("" ::: "memory");
+    rank[r] = before + __popcll(peers & lower);
+    if (e >= 0 && (peers & lower) == 0) wcnt[wave][e] = (uint16_t)(before + __popcll(peers));
+    asm volatile("" ::: "memory");
+  }
+  __syncthreads();
+  int c = 0;   // expert t's slots
+  for (int k = t; k <= E; k += 1024) {
+    int run = 0;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int x = wcnt[v][k];
+      wcnt[v][k] = (uint16_t)run;
+      run += x;
+    }
+    if (k < E) c = run;
+    else rs.status[0] = run;
+  }
+  const int order = c * MAX_E + (MAX_E - 1 - t);   // descending: by count, then ascending id
+  ord[t] = t < E ? order : -1;                     // -1: behind every expert
+  int n[N], p[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) n[j] = p[j] = t >= E ? 0 : j == 0 ? c : tiles_of(j - 1, c, rs.big_min, rs.small_bm);
+  block_exclusive_scans_1024<N>(p, sh, (E + 63) / 64);
+  if (t < E) {
+    rs.counts[t] = c;
+    rs.offsets[t] = base[t] = p[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) rs.tile_prefix[(j - 1) * (E + 1) + t] = p[j];
+    if (t == E - 1) {
+      rs.offsets[E] = base[E] = p[0] + c;
+#pragma unroll
+      for (int j = 1; j < N; ++j) rs.tile_prefix[(j - 1) * (E + 1) + E] = p[j] + n[j];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int s = (wave * R + r) * 64 + lane, e = key[r];
+    if (e < 0) continue;
+    const int pos = base[e] + wcnt[wave][e] + rank[r];
+    list[pos] = (uint16_t)s;
+    rs.inv_pos[s] = e < E ? pos : -1;
+  }
+  __syncthreads();
+  const int valid = base[E];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int pos = r * 1024 + t;
+    if (pos >= S) break;
+    const int s = list[pos];
+    rs.sorted_slot[pos] = s;
+    rs.tok_of_pos[pos] = s / K;
+    rs.w_of_pos[pos] = pos < valid && w ? w[s] : 0.f;
+  }
+  if (t < E) {
+    int r = 0;
+#pragma unroll 8
+    for (int e = 0; e < E; e += 4) {
+      const int4 q = *(const int4*)(ord + e);
+      r += (int)(q.x > order) + (int)(q.y > order) + (int)(q.z > order) + (int)(q.w > order);
+    }
+    rs.expert_order[r] = t;
   }
 }
 
@@ -337,6 +480,13 @@ hipError_t launch_router_bwd(const int32_t* ids, const float* w, const float* dw
 
 hipError_t launch_route(const int32_t* ids, const float* w, int S, int K, int E, const RouteState& rs,
                         hipStream_t stream) {
+  if (S <= ROUTE_ONE_MAX)
+    return run_kernel("route_one", stream, [&] {
+      if (S <= 1024) route_one_kernel<1><<<1, 1024, 0, stream>>>(ids, w, S, K, E, rs);
+      else if (S <= 2048) route_one_kernel<2><<<1, 1024, 0, stream>>>(ids, w, S, K, E, rs);
+      else if (S <= 4096) route_one_kernel<4><<<1, 1024, 0, stream>>>(ids, w, S, K, E, rs);
+      else route_one_kernel<8><<<1, 1024, 0, stream>>>(ids, w, S, K, E, rs);
+    });
   const int nblk = rs.nblk;
   hipError_t err = run_kernel("route_hist", stream, [&] {
     route_hist_kernel<<<nblk, ROUTE_THREADS, 0, stream>>>(ids, S, E, rs.blk_hist, rs.blk_bad);
