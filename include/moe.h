@@ -252,8 +252,8 @@ moe_status_t moe_fwd_noalloc(const moe_desc_t* desc, const void* hidden,
  * by kernels sized for one or two slots an expert.  a = phi(..) is rounded to
  * the activations' type as in moe_fwd; sums over H, I and K are fp32 in a fixed
  * order (not moe_fwd's order, so the two agree to rounding, not bit for bit).
- * Where a large bf16 layer's experts hold more than 32 slots on average it
- * runs moe_fwd's kernels instead, which are then faster.
+ * Where a bf16 layer has so many slots and weights (T K H I above 2e9) that
+ * moe_fwd's kernels are faster, it runs those.
  * MOE_ERR_UNSUPPORTED also where 64 rows of the weights, hidden, or a [S,I]
  * reach 2^31 bytes.  ws: at least moe_few_workspace_size() bytes (its first
  * word is the status that moe_check_device_status reports); nothing in it has
@@ -297,7 +297,8 @@ moe_status_t moe_mx_dequantize(const void* codes, const void* scales,
  * [E,H,I/32]; hidden, out and a = phi(..) are bf16 and products accumulate in
  * fp32.  Computes what moe_fwd computes on the weights moe_mx_dequantize
  * gives.  dtype must be MOE_BF16, H and I multiples of 32 and at most 14336,
- * and hidden below 2^31 bytes, else MOE_ERR_UNSUPPORTED.  ws: at least moe_mx_workspace_size() bytes.
+ * and hidden below 2^31 bytes, else MOE_ERR_UNSUPPORTED.  ws: at least
+ * moe_mx_workspace_size() bytes.
  * Everything else as for moe_fwd (no `saved`, no backward);
  * moe_mx_fwd_logits is to it as moe_fwd_logits to moe_fwd. */
 moe_status_t moe_mx_workspace_size(const moe_desc_t* desc, size_t* ws_bytes);

@@ -460,21 +460,29 @@ moe_status_t few_check(const Dims& d) {
   return MOE_OK;
 }
 
-// Large layers whose experts hold more than 32 slots on average: the few-token
-// kernels, which read 32 to 64 tokens' rows for every 32 to 64 weight rows, are
-// then bound by those and take the weights in several passes, and the routed
-// products are faster (us, few-token kernels against routed products):
-//   experts of H x I, tokens, top-k    slots/E   bf16        4-bit
-//    8 of 2880 x 2880, 128, 4               64   215  138    122   93
-//    8 of 2880 x 2880,  64, 4               32   132  132     75   81
-//   10 of 4096 x 2880, 128, 4               51   273  184    159  101
-//   16 of 2880 x 1440, 128, 8               64   205  129    115   94
-//    8 of 4096 x 2048, 128, 2               32   119  141     66   82
-// Small layers stay, where the routing is the larger part:
-//    8 of 2048 x 1024,  64, 8               64    53   83
-//    4 of 2048 x 2048, 128, 4              128    87   96
-//    4 of 2048 x 1024, 128, 4              128    54   82     61   56
-bool many_slots(const Dims& d) { return d.S > 32 * d.E && d.E * d.H * d.I > (int64_t(1) << 24); }
+// Calls that the routed products are faster for: the few-token kernels read 16
+// to 64 tokens' rows again for every 32 to 64 weight rows, which grows with
+// S H I, where the products pay a routing (4-bit: a launch; bf16: and products
+// made for more rows).  With 4 slots an expert or fewer both are bound by the
+// weights.  (us, few-token kernels against routed products:
+//   experts of H x I, tokens, top-k    S H I     bf16        4-bit
+//    8 of 2880 x 2880,  48, 4          1.6e9   108  118     60   66
+//    8 of 2880 x 2880,  64, 4          2.1e9   132  122     75   72
+//    8 of 4096 x 2048, 128, 2          2.1e9   119  131     67   71
+//   16 of 2880 x 1440,  64, 8          2.1e9   130  106     74   66
+//   32 of 2880 x 2880,  64, 4          2.1e9   298  300    119  127
+//   32 of 2880 x 2880, 128, 4          4.2e9   361  318    154  134
+//   16 of 2880 x 1440, 128, 8          4.2e9   205  119    115   81
+//  128 of 2880 x 2880, 128, 4          4.2e9  1015 1036    361  352
+//   16 of 2048 x 1024, 128, 4          1.1e9    76   83     49   47
+//    4 of 2048 x 1024,  64, 4          0.5e9    31   68     36   45
+//    4 of 2048 x 1024, 128, 4          1.1e9    54   72     61   46
+//    8 of  512 x  512, 128, 8          0.3e9    37   47     40   31
+// The last two: above 64 slots an expert 4-bit weights are converted once for
+// each pass of 32 tokens.)
+bool many_slots(const Dims& d, bool mx) {
+  return (d.S > 4 * d.E && d.S * d.H * d.I > 2000000000) || (mx && d.S > 64 * d.E);
+}
 
 // Microscaled 4-bit weights: whole blocks of 32 columns, bf16 activations.
 moe_status_t mx_check(const Dims& d) {
@@ -492,12 +500,12 @@ moe_status_t mx_check(const Dims& d) {
 // partial sums, within 64 KB.
 bool mx_few(const Dims& d) {
   const int64_t wide = d.H > d.I ? d.H : d.I;
-  return few_check(d) == MOE_OK && wide <= 8192 && 2 * d.S + 2 * wide <= 31 * 1024 && !many_slots(d);
+  return few_check(d) == MOE_OK && wide <= 8192 && 2 * d.S + 2 * wide <= 31 * 1024 && !many_slots(d, true);
 }
 size_t mx_ws(const Dims& d) { return mx_few(d) ? few_layout(d).end : make_layout(d).f_end; }
 
 // Whether moe_fwd_few runs moe_fwd's kernels.
-bool few_full(const Dims& d) { return d.esz == 2 && many_slots(d); }
+bool few_full(const Dims& d) { return d.esz == 2 && many_slots(d, false); }
 size_t few_ws(const Dims& d) { return few_full(d) ? make_layout(d).f_end : few_layout(d).end; }
 
 struct LayerPtrs {

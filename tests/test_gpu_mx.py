@@ -147,10 +147,10 @@ def test_large_layer_of_few_experts(T):
     mx_case(small_inputs(T, 1472, 1472, 2, 2, "bf16", "swiglu", "concat", seed=T))
 
 
-@pytest.mark.parametrize("T", [32, 33, 100])
-def test_sides_of_the_rule_of_many_slots(T):
-    """32 slots an expert and more in a layer of E H I over 2^24: the latter run the grouped products."""
-    mx_case(small_inputs(T, 1472, 1472, 8, 8, "bf16", "clamped", "interleaved", seed=T))
+@pytest.mark.parametrize("T,H,E,K", [(125, 2304, 3, 3), (128, 2304, 3, 3), (64, 160, 2, 2), (65, 160, 2, 2), (128, 96, 3, 3)])
+def test_sides_of_the_rule_of_many_slots(T, H, E, K):
+    """S H I just below and above 2e9, and 64 slots an expert and more: the latter run the grouped products."""
+    mx_case(small_inputs(T, H, H, E, K, "bf16", "clamped", "interleaved", seed=T + H))
 
 
 @pytest.mark.parametrize("T", [3, 140])
