@@ -4,8 +4,7 @@
 
 namespace moe {
 
-// Most tokens of a few-token call, and most bytes from a buffer's base that a
-// lane's 32-bit offset may name.
+// Most tokens of a few-token call.
 constexpr int FEW_MAX_T = 128;
 
 // Strides are bytes.  Gate (up) row j of expert e starts gu_es e + gu_rs j
