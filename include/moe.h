@@ -25,6 +25,7 @@
  *   MOE_SWIGLU:      g * sigmoid(g) * u
  *   MOE_CLAMPED_GLU: gc = min(g, L), uc = clamp(u, -L, L),
  *                    (uc + 1) * gc * sigmoid(alpha * gc)     (L = clamp_limit)
+ *                    (min and clamp of a NaN are NaN)
  *
  * Conventions for every entry point
  *   - All tensor pointers are DEVICE pointers, row-major, contiguous, 16-byte

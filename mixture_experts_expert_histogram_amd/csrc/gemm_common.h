@@ -30,6 +30,13 @@ template <> __device__ __forceinline__ void store_val<float>(float* p, float v) 
 // rounded to bf16 or summed in fp32 afterwards.
 __device__ __forceinline__ float sigmoid_f(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
 
+// The clamps of the clamped GLU keep a NaN: minimum and maximum here are the
+// IEEE 754-2019 operations, one instruction each (v_minimum3 / v_maximum3),
+// where v_med3 or v_min return the other operand and would turn the NaN of a
+// broken weight or activation into a plausible finite value.
+__device__ __forceinline__ float clamp_max(float x, float L) { return __builtin_elementwise_minimum(x, L); }
+__device__ __forceinline__ float clamp_both(float x, float L) { return __builtin_elementwise_maximum(clamp_max(x, L), -L); }
+
 // Gated activation (SwiGLU, ACT = 0, or the clamped GLU of the gpt-oss-shaped
 // pages, ACT = 1), with the kind fixed at compile time.
 template <int ACT>
@@ -37,8 +44,8 @@ __device__ __forceinline__ float glu_fwd_t(float g, float u, float L, float al) 
   if constexpr (ACT == 0) {
     return g * sigmoid_f(g) * u;
   } else {
-    const float gc = __builtin_amdgcn_fmed3f(g, -__builtin_inff(), L);   // min(g, L)
-    const float uc = __builtin_amdgcn_fmed3f(u, -L, L);
+    const float gc = clamp_max(g, L);
+    const float uc = clamp_both(u, L);
     return (uc + 1.f) * gc * sigmoid_f(al * gc);
   }
 }
@@ -52,12 +59,12 @@ __device__ __forceinline__ float glu_bwd_t(float g, float u, float da, float L, 
     du = da * silu;
     return silu * u;
   } else {
-    const float gc = __builtin_amdgcn_fmed3f(g, -__builtin_inff(), L);   // min(g, L)
-    const float uc = __builtin_amdgcn_fmed3f(u, -L, L);
+    const float gc = clamp_max(g, L);
+    const float uc = clamp_both(u, L);
     const float s = sigmoid_f(al * gc);
     const float q = gc * s;
     dg = (g <= L) ? da * (uc + 1.f) * s * (1.f + al * gc * (1.f - s)) : 0.f;
-    du = (uc == u) ? da * q : 0.f;   // u inside [-L, L]
+    du = (uc == u) ? da * q : 0.f;   // u inside [-L, L] (a NaN is not)
     return (uc + 1.f) * q;
   }
 }
