@@ -283,8 +283,10 @@ moe_status_t moe_fwd_few_logits(const moe_desc_t* desc, const void* hidden,
  * moe_mx_quantize: s - 127 = max(floor(log2(max |w|)) - 2, -127) over the
  * block, the code is the nearest to w / 2^(s-127), ties to the even code,
  * magnitudes beyond 6 become 6; a block with an infinity or NaN gets s = 255
- * and zero codes.  moe_mx_dequantize gives the values the codes stand for
- * (exact in bf16 and fp32).  w: [rows, cols] of `dtype` (moe_dtype_t); cols a
+ * and zero codes.  moe_mx_dequantize gives the values the codes stand for:
+ * exact in bf16 and fp32, except that a value of 2^128 and more (scale byte
+ * 253 with |c| of 4 and 6, 254 with 2 and more; moe_mx_quantize writes neither
+ * byte) is infinite in both.  w: [rows, cols] of `dtype` (moe_dtype_t); cols a
  * multiple of 32, else MOE_ERR_UNSUPPORTED; rows = 0 does nothing. */
 moe_status_t moe_mx_quantize(const void* w, int32_t dtype, int64_t rows,
                              int64_t cols, void* codes, void* scales,

@@ -535,7 +535,8 @@ def mx_quantize(w, out=None):
 
 
 def mx_dequantize(codes, scales, dtype="bf16", out=None):
-    """The values that codes [..., C/2] and scales [..., C/32] stand for, as bf16 or fp32 [..., C] (exact)."""
+    """The values that codes [..., C/2] and scales [..., C/32] stand for, as bf16 or fp32 [..., C]: exact,
+    but infinite from 2^128 on (scale bytes 253 and 254, which mx_quantize does not write)."""
     import torch
     if not codes.is_cuda or codes.dim() < 1:
         raise ValueError("mx_dequantize takes device tensors")

@@ -15,8 +15,8 @@ __device__ __forceinline__ float mx_scale(uint32_t s) {
   return __builtin_bit_cast(float, s == 0 ? 0x00400000u : s == 255 ? 0x7fc00000u : s << 23);
 }
 
-// Four bytes of codes (8 elements) as bf16 (exact: 2 significant bits), times
-// the block's scale.
+// Four bytes of codes (8 elements) as bf16, times the block's scale: exact (2
+// significant bits, subnormals included), infinite from 2^128 on.
 __device__ __forceinline__ bf16x8_t mx_expand(uint32_t codes, float scale) {
   struct { bf16x2_t p[4]; } r;
   r.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);

@@ -108,7 +108,8 @@ __global__ __launch_bounds__(Q_THREADS) void mx_dequantize_kernel(const uint32_t
       const long i = i0 + u * Q_THREADS;
       if (i >= n8) continue;
       // the product is exact: a code has 2 significant bits, and 2^-127 times
-      // the smallest one, 0.5, is a subnormal of both types
+      // the smallest one, 0.5, is a subnormal of both types (from 2^128 on,
+      // bytes 253 and 254, it is infinite in both)
       const float sc = mx_scale(s[u]);
       float y[8];
 #pragma unroll
