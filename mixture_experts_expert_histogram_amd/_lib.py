@@ -389,14 +389,18 @@ def _raw_stream(index: int) -> int:
     return q(index) if q is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-def _launch(device, where: str, f, *args):
-    """Call f(*args, stream) on the current stream of the tensors' device."""
+def _on_device(device, f, *args) -> int:
+    """f(*args, stream) with the tensors' device current and its current stream; returns the status."""
     import torch
     if device.index == torch.cuda.current_device():
-        status = f(*args, _raw_stream(device.index))
-    else:
-        with torch.cuda.device(device):
-            status = f(*args, _raw_stream(device.index))
+        return f(*args, _raw_stream(device.index))
+    with torch.cuda.device(device):
+        return f(*args, _raw_stream(device.index))
+
+
+def _launch(device, where: str, f, *args):
+    """Call f(*args, stream) on the current stream of the tensors' device."""
+    status = _on_device(device, f, *args)
     if status != MOE_OK:
         raise MoeError(status, where)
 
@@ -592,8 +596,8 @@ def mx_fwd_logits(hidden, logits, K: int, gate_up, down, act="swiglu", layout="c
 
 
 def check_device_status(ws) -> int:
-    """Synchronises the current stream; returns the status code of the last routing in ws."""
-    return library().moe_check_device_status(_ptr(ws), _stream())
+    """Synchronises the current stream of ws's device; returns the status code of the last routing in ws."""
+    return _on_device(ws.device, library().moe_check_device_status, _ptr(ws))
 
 
 def timing_enable(max_launches: int = 4096):
