@@ -249,12 +249,13 @@ moe_status_t moe_fwd_noalloc(const moe_desc_t* desc, const void* hidden,
 
 /* Forward for a few tokens (decoding): T <= MOE_FEW_MAX_TOKENS, else
  * MOE_ERR_UNSUPPORTED.  Computes moe_fwd's out without its routing pass and
- * without `saved` (no backward): each active expert's weights are read once,
- * by kernels sized for one or two slots an expert.  a = phi(..) is rounded to
- * the activations' type as in moe_fwd; sums over H, I and K are fp32 in a fixed
- * order (not moe_fwd's order, so the two agree to rounding, not bit for bit).
- * Where a bf16 layer has so many slots and weights (T K H I above 2e9) that
- * moe_fwd's kernels are faster, it runs those.
+ * without `saved` (no backward), by kernels sized for one or two slots an
+ * expert: an active expert's weights are read once for each 64 of its slots.
+ * a = phi(..) is rounded to the activations' type as in moe_fwd; sums over H,
+ * I and K are fp32 in a fixed order (not moe_fwd's order, so the two agree to
+ * rounding, not bit for bit).  A bf16 call with more than 4 slots an expert
+ * (T K > 4 E) and T K H I above 2e9 runs moe_fwd's kernels, with their order
+ * and workspace.
  * MOE_ERR_UNSUPPORTED also where 64 rows of the weights, hidden, or a [S,I]
  * reach 2^31 bytes.  ws: at least moe_few_workspace_size() bytes (its first
  * word is the status that moe_check_device_status reports); nothing in it has
@@ -302,6 +303,11 @@ moe_status_t moe_mx_dequantize(const void* codes, const void* scales,
  * gives.  dtype must be MOE_BF16, H and I multiples of 32 and at most 14336,
  * and hidden below 2^31 bytes, else MOE_ERR_UNSUPPORTED.  ws: at least
  * moe_mx_workspace_size() bytes.
+ * Up to MOE_FEW_MAX_TOKENS tokens run as in moe_fwd_few, an expert's weights
+ * read once for each 32 of its slots.  Grouped products over routed slots run
+ * more tokens, and of those calls the ones with T K > 4 E and T K H I above
+ * 2e9, with T K > 64 E, with H or I above 8192, or with T K + max(H, I) above
+ * 15872.  The two sum in different orders and need different workspaces.
  * Everything else as for moe_fwd (no `saved`, no backward);
  * moe_mx_fwd_logits is to it as moe_fwd_logits to moe_fwd. */
 moe_status_t moe_mx_workspace_size(const moe_desc_t* desc, size_t* ws_bytes);

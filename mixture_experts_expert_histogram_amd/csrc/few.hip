@@ -7,7 +7,8 @@
 //   out[t] = sum_k y[t K + k]
 //
 // With a few tokens an expert holds one or two slots, and the time is that of
-// reading the active experts' weights once: 2 flops a weight byte against the
+// reading the active experts' weights once (again for each 64 of an expert's
+// slots, 32 on 4-bit weights): 2 flops a weight byte against the
 // 300 where the matrix cores would bound it.  So nothing here is staged for
 // reuse: a wave reads its weight rows (32 of plain weights, 64 of 4-bit ones)
 // straight into matrix-core fragments (16 rows by k, every lane 16 bytes of one
@@ -42,8 +43,9 @@ constexpr uint32_t kPast = 0x80000000u;   // byte offset past every buffer
 
 // A unit of a weight row's k: WQ times 64 bytes, of which a lane holds 16.
 // XQ: 16-byte loads of a token row for the same k; XSZ: bytes a token element.
-// Plain weights go by whole cache lines (units of 64 bytes, taken by two waves,
-// read 16 tokens' gpt-oss-shaped layer in 486 us instead of 456).
+// Plain weights go by whole cache lines (16 tokens' gpt-oss-shaped layer: 420 us;
+// in units of 64 bytes, a line's halves to two waves, 473, and 478 with twice
+// the units in flight).
 template <int KIND> struct Unit;
 template <> struct Unit<W_BF16> { static constexpr int K = 64, WQ = 2, XQ = 2, XSZ = 2; };
 template <> struct Unit<W_F32> { static constexpr int K = 32, WQ = 2, XQ = 2, XSZ = 4; };
@@ -526,8 +528,11 @@ __global__ __launch_bounds__(256) void few_combine_kernel(FewArgs p) {
 // One token's slots are K experts' rows with one column, so no list is
 // needed; its two kernels are the whole layer.  128 experts of 2880 x 2880,
 // top-4, from logits: bf16 29 us for 133 MB (4.6 TB/s) and 17 us for 66 MB (3.9
-// TB/s), 4-bit 13 and 9 us: bound by the kernels' ramps, from the launch to
-// the first bytes and from the last ones to the end.
+// TB/s), 4-bit 13 and 9 us.  Neither rate is the memory's.  A wave of 4-bit
+// weights has one unit in flight and waits for it 6 times in the gate_up kernel
+// and 12 times in the down kernel (K of 2880), and the down kernel's 180
+// workgroups leave 76 of the 256 CUs idle; how much of the time is those waits
+// and how much the launches' start and end has not been measured.
 //
 // The choice from logits: an expert's rank is the number of better ones (a
 // larger logit, or an equal one with a lower id; NaN is never chosen), counted

@@ -1,6 +1,7 @@
-// Grouped products on microscaled 4-bit expert weights, for more tokens than
-// the few-token kernels take: the gate_up projection with its activation and
-// the down projection with the routing weight, over the routed positions.
+// Grouped products on microscaled 4-bit expert weights, for the calls that the
+// few-token kernels do not take (more than 128 tokens, many slots an expert,
+// long rows; the rule is in api.cpp): the gate_up projection with its activation
+// and the down projection with the routing weight, over the routed positions.
 //
 // One workgroup (4 waves) computes BM = 32 or 64 positions x 256 weight
 // rows of one expert on v_mfma_f32_16x16x32_bf16, BM x 64 a wave, fp32
@@ -65,7 +66,10 @@ struct MxCfg {
   static constexpr int HALF = BM * 64;     // elements of a stage's 64-k half
   static constexpr int NB = BM / 8 / NW;   // 1 KB loads of a wave per half (8 rows of 128 bytes)
   static constexpr int LS = BM == 32 ? 4 : 2;   // stages whose codes of a row are loaded together
-  static constexpr int OCC = 2;   // waves a SIMD that the registers allow for
+  // Waves a SIMD that the registers allow for: 231 of 256 with 32 positions, 254
+  // (down) and 256 (gate_up) with 64, where two values are spilled around one of
+  // the loops and none inside a loop.
+  static constexpr int OCC = 2;
 };
 
 // A raw buffer of 2^31 bytes at p (wave-uniform) as its four descriptor words.
@@ -312,7 +316,7 @@ __global__ __launch_bounds__(C::NT, C::OCC) void mx_gemm_kernel(MxArgs p) {
   const GArgs& g = p.g;
   int e, m0, rows, nt;
   if (!row_tile<C::BM>(g, e, m0, rows, nt)) return;
-  {   // an expert's tiles share its positions evenly: one over 128 is two tiles of 65, not 128 and 1
+  {   // an expert's tiles share its positions evenly, in blocks of 16: 72 on tiles of 64 are 48 and 24, not 64 and 8
     const int off = g.offsets[e], n = g.offsets[e + 1] - off, tiles = (n + C::BM - 1) / C::BM;
     const int share = ((n + tiles - 1) / tiles + 15) & ~15, mt = (m0 - off) / C::BM;
     m0 = off + mt * share;
@@ -444,7 +448,9 @@ hipError_t launch(const GemmProblem& pb, MxArgs p, const char* name, hipStream_t
 // tokens 503 us against 516, 4096 tokens 0.98 ms against 1.14).  Tiles of
 // 128 positions x 512 rows on 8 waves move a third less through the load path,
 // but one workgroup a CU leaves its waits and its ends uncovered: 1.01 ms at
-// 4096 tokens, 3.32 against 3.37 ms at 16384.
+// 4096 tokens, 3.32 against 3.37 ms at 16384.  The average decides for every
+// expert: with Zipf(1.2) routing, whose largest expert has 382 of 2048 slots
+// (3063 of 16384), 512 tokens take 428 us (uniform 414) and 4096 1.00 ms (0.98).
 template <bool GATE_UP>
 hipError_t launch_by_rows(const GemmProblem& pb, const MxArgs& p, const char* name, hipStream_t s) {
   if ((long)pb.S <= 16L * pb.E) return launch<MxCfg<32>, GATE_UP>(pb, p, name, s);
