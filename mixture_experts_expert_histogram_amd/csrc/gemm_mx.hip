@@ -3,6 +3,9 @@
 // long rows; the rule is in api.cpp): the gate_up projection with its activation
 // and the down projection with the routing weight, over the routed positions.
 //
+// The activation is rounded to bf16, the second product's operand type; every
+// sum and the down product's rows are fp32.
+//
 // One workgroup (4 waves) computes BM = 32 or 64 positions x 256 weight
 // rows of one expert on v_mfma_f32_16x16x32_bf16, BM x 64 a wave, fp32
 // accumulators.
