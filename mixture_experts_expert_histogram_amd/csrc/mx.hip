@@ -1,9 +1,11 @@
 // Weight rows to 4-bit microscaled floating point and back (the format of
 // mx.h).  Rows are whole blocks of 32, so a tensor is one run of blocks.
 //
-// Both directions move each byte once and are bound by HBM: 265 M bf16 elements
-// (531 + 133 + 8 MB) are quantised in 97 us and dequantised in 94, 6.9 and 7.1
-// TB/s, a million fp32 ones in 3 us each, which is a launch.  A thread takes 8
+// Both directions move each byte once: 265 M bf16 elements (531 + 133 + 8 MB)
+// are quantised in 97 us and dequantised in 94, 6.9 and 7.1 TB/s, which is HBM's
+// rate, a million fp32 ones in 3 us each, which is a launch, and 265 M fp32 ones
+// (1062 + 141 MB) in 220 and 453, where a lane's 32 bytes are stored 16 at a
+// time, half lines of a wave's run.  A thread takes 8
 // elements (16 bytes of bf16, 32 of fp32, 4 bytes of codes), so that a wave's
 // accesses are contiguous in every tensor; the 4 threads of a block find its
 // largest magnitude by two quad permutes.
