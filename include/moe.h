@@ -323,6 +323,144 @@ moe_status_t moe_mx_fwd_logits(const moe_desc_t* desc, const void* hidden,
                                int32_t* topk_ids, float* topk_weights,
                                void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ---- The operators around the routed experts.  Same conventions as above:
+ * device pointers, row-major, contiguous, 16-byte aligned, every buffer the
+ * caller's, asynchronous on `stream`, nothing launched after an error. */
+
+/* Gated feed-forward block that every token passes: the shared expert beside
+ * the routed ones, or a dense layer.
+ *   out[t] = add[t] + s_t * Wd . phi(Wgu . x_t),   s_t = sigmoid(gate[t])
+ * with the descriptor's phi, gate/up layout and types; its E and K must be 1
+ * (else MOE_ERR_INVALID_ARG).  x, out, add [T,H]; w_gate_up [2I,H]; w_down
+ * [H,I]; gate fp32 [T].  add may be NULL (zero) and may be out; gate may be
+ * NULL (s = 1).
+ *   - H and I at most 2^20 and H I at most 2^28, else MOE_ERR_UNSUPPORTED.
+ *   - a = phi(..) is rounded to the activations' type as the second product's
+ *     operand; sums are fp32; out is rounded once.
+ *   - Up to 64 tokens without `saved` run on kernels that read the weights
+ *     once and make no tiles; their order of sums is their own.
+ *   - `saved` (nullable) receives the gate and up values (fp32, in an order of
+ *     the library's) for moe_ffn_bwd; saved_bytes below the required size:
+ *     MOE_ERR_WORKSPACE.
+ * moe_ffn_bwd, given d_out [T,H]: d_x [T,H], d_gate fp32 [T] (with gate;
+ * s (1 - s) <d_out, y>), d_w_gate_up [2I,H], d_w_down [H,I] in grad_dtype
+ * (fp32 sums over the tokens); the gradient of add is d_out.  `saved`: what
+ * moe_ffn_fwd left for the same inputs, or NULL (recomputed).  T = 0 writes
+ * zero weight gradients.  In fp32 the products of more than 64 tokens, and
+ * the backward pass, are those of moe_fwd / moe_bwd with one expert.
+ * Any output of moe_ffn_workspace_size may be NULL. */
+moe_status_t moe_ffn_workspace_size(const moe_desc_t* desc, size_t* fwd_ws,
+                                    size_t* bwd_ws, size_t* saved_bytes);
+moe_status_t moe_ffn_fwd(const moe_desc_t* desc, const void* x,
+                         const void* w_gate_up, const void* w_down,
+                         const float* gate, const void* add, void* out,
+                         void* saved, size_t saved_bytes, void* ws,
+                         size_t ws_bytes, hipStream_t stream);
+moe_status_t moe_ffn_bwd(const moe_desc_t* desc, const void* x,
+                         const void* w_gate_up, const void* w_down,
+                         const float* gate, const void* d_out,
+                         const void* saved, size_t saved_bytes, void* d_x,
+                         float* d_gate, void* d_w_gate_up, void* d_w_down,
+                         void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Norms around a block, rms(v)^2 = mean(v^2) + eps over a row, all in fp32
+ * from the stored values, rounded once.
+ *   moe_norm_fwd:      y = w * x / rms(x)
+ *   moe_norm_bwd:      d_x = d_add + its gradient for d_y;  d_w fp32 [H]
+ *   moe_residual_fwd:  n = w_post * h / rms(h)  (n = h if w_post is NULL)
+ *                      x_new = x + scale * gate * n
+ *                      y = w_next * x_new / rms(x_new), from x_new before it
+ *                      is rounded  (w_next NULL: y is not written)
+ *   moe_residual_bwd:  given d_x_new and d_y, and x_new as it was stored,
+ *                      t = d_x_new + the norm's gradient for d_y;
+ *                      d_x = t, d_h, d_gate, d_w_post, d_w_next of the above
+ * x, h, x_new, y and their gradients [T,H] and the weights [H] have the
+ * descriptor's dtype; d_w, d_w_post, d_w_next are fp32 [H].
+ * gate, of that dtype, is [T] (MOE_GATE_ROW: one value for a row), [H]
+ * (MOE_GATE_COLUMN) or [T,H] (MOE_GATE_FULL); d_gate has its shape, fp32 for
+ * the two that are sums, the descriptor's dtype for MOE_GATE_FULL.
+ * NULL is allowed for d_add and d_x_new (zero), w_post and w_next (no such
+ * norm; its gradient's pointer is then ignored, as d_y is without w_next), and
+ * gate with MOE_GATE_NONE.  x_new may be x, and d_x may be d_add or d_x_new.
+ * H a multiple of 8, at most 16384, else MOE_ERR_UNSUPPORTED; T < 2^31.
+ * T = 0 writes zeros to the weights' (and a column gate's) gradients.
+ * ws (backward): moe_norm_workspace_size() bytes.  Deterministic. */
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_ROW = 1,
+  MOE_GATE_COLUMN = 2,
+  MOE_GATE_FULL = 3
+} moe_gate_t;
+typedef struct {
+  int64_t T, H;
+  int32_t dtype;     /* moe_dtype_t */
+  int32_t gate_kind; /* moe_gate_t; MOE_GATE_NONE for moe_norm_* */
+  float scale;       /* of the residual step */
+  float eps;         /* >= 0 */
+} moe_norm_desc_t;
+moe_status_t moe_norm_workspace_size(const moe_norm_desc_t* desc,
+                                     size_t* bwd_ws);
+moe_status_t moe_norm_fwd(const moe_norm_desc_t* desc, const void* x,
+                          const void* w, void* y, hipStream_t stream);
+moe_status_t moe_norm_bwd(const moe_norm_desc_t* desc, const void* x,
+                          const void* w, const void* d_y, const void* d_add,
+                          void* d_x, float* d_w, void* ws, size_t ws_bytes,
+                          hipStream_t stream);
+moe_status_t moe_residual_fwd(const moe_norm_desc_t* desc, const void* x,
+                              const void* h, const void* w_post,
+                              const void* gate, const void* w_next,
+                              void* x_new, void* y, hipStream_t stream);
+moe_status_t moe_residual_bwd(const moe_norm_desc_t* desc, const void* x_new,
+                              const void* h, const void* w_post,
+                              const void* gate, const void* w_next,
+                              const void* d_x_new, const void* d_y, void* d_x,
+                              void* d_h, void* d_gate, float* d_w_post,
+                              float* d_w_next, void* ws, size_t ws_bytes,
+                              hipStream_t stream);
+
+/* Newton-Schulz orthogonalisation of E stacked M x N updates (moe_bwd's
+ * weight gradients are such stacks):
+ *   X = G / (|G| + eps), then `steps` times
+ *   X <- a X + b (X X^T) X + c (X X^T)^2 X
+ * with |G| the 2-norm of a matrix's elements, which drives the singular values
+ * towards one.  moe_orthogonalize writes X to out (out_dtype).  moe_muon_step
+ * takes a gradient G, a momentum fp32 and weights (w_dtype), [E,M,N] each:
+ *   m_out = momentum m + G,  U = G + momentum m_out (nesterov) or m_out
+ *   w_out = (1 - decay) w - lr X(U)
+ * m_out may be m and w_out may be w.
+ * Iterates are fp16 (11 bits) with fp32 sums, so X is about 1e-3 from the
+ * exact iteration in the 2-norm before it is rounded to its type; the norm is
+ * summed in 64 bits.  Coefficients must keep the iterates' singular values,
+ * which start at most 1, at most 3 and b x + c x^2 at most 14.6 in size over
+ * their squares (checked; the usual 3.4445, -4.775, 2.0315 reach 1.21 and
+ * 2.81), else MOE_ERR_UNSUPPORTED.  A NaN or infinity makes its matrix's X
+ * NaN; a zero matrix stays zero.
+ * M and N multiples of 8, at most 2^20, E at most 65535, 1 to 64 steps, else
+ * MOE_ERR_UNSUPPORTED (negative E, M or N, M or N of 0, eps or dtypes that do
+ * not exist: MOE_ERR_INVALID_ARG).  E = 0 does nothing. */
+typedef struct {
+  int64_t E, M, N;
+  int32_t dtype;     /* of G: moe_dtype_t */
+  int32_t out_dtype; /* of out, or of w and w_out */
+  int32_t steps;
+  float a, b, c;
+  float eps;         /* >= 0 */
+} moe_ortho_desc_t;
+typedef struct {
+  float lr, momentum, decay;
+  int32_t nesterov; /* 0 or 1 */
+} moe_muon_t;
+moe_status_t moe_ortho_workspace_size(const moe_ortho_desc_t* desc,
+                                      size_t* ws_bytes);
+moe_status_t moe_orthogonalize(const moe_ortho_desc_t* desc, const void* g,
+                               void* out, void* ws, size_t ws_bytes,
+                               hipStream_t stream);
+moe_status_t moe_muon_step(const moe_ortho_desc_t* desc,
+                           const moe_muon_t* opt, const void* w,
+                           const void* g, const float* m, void* w_out,
+                           float* m_out, void* ws, size_t ws_bytes,
+                           hipStream_t stream);
+
 /* Synchronises `stream` and reports MOE_ERR_BAD_EXPERT_ID if the last
  * routing done in `ws` met an id outside [0,E), else MOE_OK. */
 moe_status_t moe_check_device_status(const void* ws, hipStream_t stream);

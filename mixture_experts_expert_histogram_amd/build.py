@@ -12,7 +12,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB_NAME = "libmoe_mi355x.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = ["route.hip", "gemm.hip", "gemm_dma.hip", "gemm_mx.hip", "few.hip", "mx.hip", "api.cpp"]
+SOURCES = ["route.hip", "gemm.hip", "gemm_dma.hip", "gemm_mx.hip", "few.hip", "mx.hip", "ffn_fwd.hip",
+           "ffn_bwd.hip", "ffn_few.hip", "norm.hip", "ortho.hip", "api.cpp", "api_block.cpp"]
 ARCH = "gfx950"
 
 

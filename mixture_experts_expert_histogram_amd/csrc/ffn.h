@@ -1,0 +1,56 @@
+// Arguments and launches of the gated feed-forward block (ffn_fwd.hip,
+// ffn_bwd.hip, ffn_few.hip).
+#pragma once
+#include "moe_internal.h"
+
+namespace moe {
+
+// Most tokens that the kernels for a few tokens take (weights read once, no
+// tiles); more go to the dense products.
+constexpr int FFN_FEW_T = 64;
+
+struct FfnArgs {
+  const void* x;        // [T,H]
+  const void* gu_g;     // gate row j starts gu_rs j elements after gu_g, up row j after gu_u
+  const void* gu_u;
+  const void* gu;       // [2I,H], the rows in the layout's order
+  const void* wd;       // [H,I]
+  const float* gate;    // [T] logits, or null
+  const void* add;      // [T,H], or null
+  const void* dout;     // [T,H]
+  void* a;              // [T,I]
+  float* z;             // gate and up values in blocks (z_block), or null
+  void* out;            // [T,H]
+  void* dz;             // [T,2I] in the layout's order
+  void* aw;             // [T,I]: sigmoid(gate) a
+  void* dx;             // [T,H]
+  float* dgate;         // [T], or null
+  float* part;          // [T,parts]
+  void* dgu;            // [2I,H]
+  void* dwd;            // [H,I]
+  long gu_rs;
+  int T, H, I;
+  int act, layout, grad_f32;
+  float limit, alpha;
+  int mt, nt, parts;    // tiles of the present product; partial sums of a row
+};
+static_assert(sizeof(void*) == 8 && sizeof(long) == 8, "64-bit pointers and longs on host and device");
+
+// Floats of the saved gate and up values: blocks of 32 rows x 8 columns.
+inline size_t ffn_z_floats(int64_t T, int64_t I) { return (size_t)((T + 31) / 32) * 32 * I * 2; }
+// Most partial sums of a row that ffn_down_dgrad writes.
+inline int64_t ffn_parts(int64_t I) { return 2 * ((I + 63) / 64); }
+
+hipError_t launch_ffn_gate_up(FfnArgs p, hipStream_t s);      // a (if not null) and z (if not null)
+hipError_t launch_ffn_down(FfnArgs p, hipStream_t s);         // out
+hipError_t launch_ffn_down_dgrad(FfnArgs p, hipStream_t s);   // dz, aw, dgate
+hipError_t launch_ffn_gate_up_dgrad(FfnArgs p, hipStream_t s);   // dx
+hipError_t launch_ffn_wgrads(FfnArgs p, hipStream_t s);       // dgu, dwd
+hipError_t launch_ffn_few(int dtype, FfnArgs p, hipStream_t s);  // out, by way of a
+// ids[t] = 0 and w[t] = sigmoid(gate[t]) (1 without a gate): the block as a layer of one expert
+hipError_t launch_ffn_one_expert(const float* gate, int T, int32_t* ids, float* w, hipStream_t s);
+hipError_t launch_ffn_add(const float* add, const float* y, long n, float* out, hipStream_t s);   // out = add + y
+// dgate[t] = w (1 - w) dw[t]
+hipError_t launch_ffn_dgate(const float* w, const float* dw, int T, float* dgate, hipStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,178 @@
+// The gated feed-forward block for up to 64 tokens, bf16 or fp32: the time is
+// that of reading 3 H I weights once, and for one token that of two launches and
+// their first loads.
+//
+// A workgroup takes 16 weight rows (8 gate and 8 up rows, or 16 rows of Wd);
+// its 8 waves split k in units of one 128-byte line a row, read straight into
+// matrix-core fragments (16 rows x 64 contiguous bytes a load) against 16 token
+// columns, D units in flight a wave.  The partial sums meet in LDS in wave order.
+// Few rows a workgroup and all of its loads in flight at once are what fills
+// the card with one matrix of 2880 x 2880.
+#include "ffn_tiles.h"
+
+namespace moe {
+namespace dense {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int FEW_NW = 8;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p) {
+  const uint64_t v = (uint64_t)(uintptr_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc((void*)(uintptr_t)(((uint64_t)hi << 32) | lo), 0, (int)kNone, 0x00027000);
+}
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+// Units of NT x 16 token columns that fit in registers.
+template <int NT> struct Depth { static constexpr int D = NT == 1 ? 6 : NT == 2 ? 4 : 2; };
+
+// The dot products of this wave's units with 16 weight rows (byte offset wrow
+// of this lane's row, lane % 16, from w) and NT x 16 tokens (rows of K elements
+// from x), left in LDS: red[wave][token][row].
+template <bool F32, int NT>
+__device__ __forceinline__ void few_dot(__amdgpu_buffer_rsrc_t w, uint32_t wrow, __amdgpu_buffer_rsrc_t x, int T, int K,
+                                        float* red, int wave, int lane) {
+  constexpr int ESZ = F32 ? 4 : 2, D = Depth<NT>::D;
+  const uint32_t bytes = (uint32_t)K * ESZ;
+  const uint32_t mine = (lane >> 4) * 16;
+  uint32_t xrow[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int t = n * 16 + (lane & 15);
+    xrow[n] = t < T ? t * bytes : kNone;
+  }
+  struct Unit { u32x4 w[2], x[NT][2]; } ring[D];
+  const auto load = [&](int u, Unit& r) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t o = u * 128 + q * 64 + mine;
+      r.w[q] = load16(w, o < bytes ? wrow + o : kNone);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) r.x[n][q] = load16(x, o < bytes && xrow[n] != kNone ? xrow[n] + o : kNone);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(wave + d * FEW_NW, ring[d]);
+  f32x4 acc[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int units = (int)((bytes + 127) / 128);
+  for (int u = wave; u < units; u += D * FEW_NW) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (F32) {
+            const f32x4 wf = __builtin_bit_cast(f32x4, ring[d].w[q]), xf = __builtin_bit_cast(f32x4, ring[d].x[n][q]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[i], xf[i], acc[n], 0, 0, 0);
+          } else {
+            acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, ring[d].w[q]),
+                                                             __builtin_bit_cast(bf16x8_t, ring[d].x[n][q]), acc[n], 0, 0, 0);
+          }
+        }
+      load(u + (d + D) * FEW_NW, ring[d]);
+      __builtin_amdgcn_sched_barrier(0);   // or every product of the ring moves before its reloads
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    *(f32x4*)(red + ((wave * NT + n) * 16 + (lane & 15)) * 16 + 4 * (lane >> 4)) = acc[n];
+  __syncthreads();
+}
+template <int NT>
+__device__ __forceinline__ float few_sum(const float* red, int t, int row) {
+  float v = 0.f;
+#pragma unroll
+  for (int w = 0; w < FEW_NW; ++w) v += red[(w * NT * 16 + t) * 16 + row];
+  return v;
+}
+
+template <bool F32, int NT>
+__global__ __launch_bounds__(FEW_NW * 64) void ffn_few_gate_up_kernel(FfnArgs p) {
+  using T = std::conditional_t<F32, float, uint16_t>;
+  __shared__ __align__(16) float red[FEW_NW * NT * 256];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int j0 = blockIdx.x * 8;
+  const long row = p.gu_rs * sizeof(T);
+  // I is a multiple of 8: the workgroup's 8 columns exist
+  const uint32_t wrow = (uint32_t)((lane & 7) * row) + (lane & 8 ? (uint32_t)((const char*)p.gu_u - (const char*)p.gu_g) : 0u);
+  few_dot<F32, NT>(rsrc((const char*)p.gu_g + row * j0), wrow, rsrc(p.x), p.T, p.H, red, wave, lane);
+  for (int o = threadIdx.x; o < 8 * p.T; o += FEW_NW * 64) {
+    const int j = o & 7, t = o >> 3;
+    store_val<T>((T*)p.a + (size_t)t * p.I + j0 + j,
+                 glu_fwd(few_sum<NT>(red, t, j), few_sum<NT>(red, t, 8 + j), p.act, p.limit, p.alpha));
+  }
+}
+
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(uint16_t v) { return __builtin_bit_cast(float, (uint32_t)v << 16); }
+
+template <bool F32, int NT>
+__global__ __launch_bounds__(FEW_NW * 64) void ffn_few_down_kernel(FfnArgs p) {
+  using T = std::conditional_t<F32, float, uint16_t>;
+  __shared__ __align__(16) float red[FEW_NW * NT * 256];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h0 = blockIdx.x * 16;
+  const uint32_t row = p.I * sizeof(T);
+  few_dot<F32, NT>(rsrc((const char*)p.wd + (size_t)row * h0), row * min(lane & 15, p.H - 1 - h0), rsrc(p.a), p.T, p.I, red,
+                   wave, lane);
+  for (int o = threadIdx.x; o < 16 * p.T; o += FEW_NW * 64) {
+    const int h = o & 15, t = o >> 4;
+    if (h0 + h >= p.H) continue;
+    const size_t at = (size_t)t * p.H + h0 + h;
+    const float ad = p.add ? as_float(((const T*)p.add)[at]) : 0.f;
+    store_val<T>((T*)p.out + at, ad + row_gate(p.gate, t) * few_sum<NT>(red, t, h));
+  }
+}
+
+template <bool F32, int NT>
+hipError_t run_few(const FfnArgs& p, hipStream_t s) {
+  const hipError_t e = run_kernel("ffn_few_gate_up", s, [&] { ffn_few_gate_up_kernel<F32, NT><<<p.I / 8, FEW_NW * 64, 0, s>>>(p); });
+  if (e != hipSuccess) return e;
+  return run_kernel("ffn_few_down", s, [&] { ffn_few_down_kernel<F32, NT><<<(p.H + 15) / 16, FEW_NW * 64, 0, s>>>(p); });
+}
+
+// ------------------------------------------------------------------ the block as one expert (fp32, many tokens)
+__global__ __launch_bounds__(256) void ffn_one_expert_kernel(const float* gate, int T, int32_t* ids, float* w) {
+  const int t = blockIdx.x * 256 + threadIdx.x;
+  if (t >= T) return;
+  ids[t] = 0;
+  w[t] = row_gate(gate, t);
+}
+__global__ __launch_bounds__(256) void ffn_add_kernel(const float* add, const float* y, long n4, float* out) {
+  for (long i = blockIdx.x * 256l + threadIdx.x; i < n4; i += gridDim.x * 256l)
+    *(f32x4*)(out + 4 * i) = *(const f32x4*)(add + 4 * i) + *(const f32x4*)(y + 4 * i);
+}
+__global__ __launch_bounds__(256) void ffn_dgate_kernel(const float* w, const float* dw, int T, float* dgate) {
+  const int t = blockIdx.x * 256 + threadIdx.x;
+  if (t < T) dgate[t] = w[t] * (1.f - w[t]) * dw[t];
+}
+
+}  // namespace dense
+
+using namespace dense;
+
+hipError_t launch_ffn_few(int dtype, FfnArgs p, hipStream_t s) {
+  if (dtype == 0) return p.T <= 16 ? run_few<false, 1>(p, s) : p.T <= 32 ? run_few<false, 2>(p, s) : run_few<false, 4>(p, s);
+  return p.T <= 16 ? run_few<true, 1>(p, s) : p.T <= 32 ? run_few<true, 2>(p, s) : run_few<true, 4>(p, s);
+}
+
+hipError_t launch_ffn_one_expert(const float* gate, int T, int32_t* ids, float* w, hipStream_t s) {
+  return run_kernel("ffn_one_expert", s, [&] { ffn_one_expert_kernel<<<(T + 255) / 256, 256, 0, s>>>(gate, T, ids, w); });
+}
+hipError_t launch_ffn_add(const float* add, const float* y, long n, float* out, hipStream_t s) {
+  const long g = (n / 4 + 255) / 256;
+  return run_kernel("ffn_add", s, [&] { ffn_add_kernel<<<(int)(g < 4096 ? g : 4096), 256, 0, s>>>(add, y, n / 4, out); });
+}
+hipError_t launch_ffn_dgate(const float* w, const float* dw, int T, float* dgate, hipStream_t s) {
+  return run_kernel("ffn_dgate", s, [&] { ffn_dgate_kernel<<<(T + 255) / 256, 256, 0, s>>>(w, dw, T, dgate); });
+}
+
+}  // namespace moe

@@ -1,0 +1,128 @@
+// Forward products of the gated feed-forward block:
+//
+//   a = phi(x Wg^T, x Wu^T),   out = add + sigmoid(gate) (a Wd^T)
+//
+// a is rounded to bf16 as the second product's operand (2.35e-3 from 64 bits in
+// the 2-norm, 1.66e-3 by the output's own rounding); the gate and up values are
+// kept in fp32 for the backward pass.
+#include "ffn_tiles.h"
+
+namespace moe {
+namespace dense {
+
+// Tile rows of B take gate and up rows in turns of 8, so that accumulator
+// groups v / 4 = 0, 2 are gate and 1, 3 up values of the same 8 columns and phi
+// needs no exchange between lanes.
+template <class C, bool A, bool Z>
+__global__ __launch_bounds__(256, 1) void ffn_gate_up_kernel(FfnArgs p) {
+  FFN_PROLOGUE(C)
+  const int j0 = nt * (C::BN / 2);
+  KSrc<C::NBA> as;
+  KSrc<C::NBB, true> bs;
+  init_rows(as, p.x, m0, p.T, p.H, wave, lane);
+  const long at = p.gu_rs * j0;
+  bs.init((const uint16_t*)p.gu_g + at, (const uint16_t*)p.gu_u + at,
+          [&](int r) { return (uint32_t)(min(((r >> 4) << 3) + (r & 7), p.I - 1 - j0) * (int)p.gu_rs * 2); }, wave, lane);
+  mainloop<C, bf16x8_t>(as, bs, p.H, lds, acc, wave, lane);
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+    const int row0 = m0 + wm * 32 * C::FM + 32 * i, row = row0 + (lane & 31);
+    if (row0 >= p.T) break;
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      const int c = j0 + (wn * C::FN + j) * 16;
+      if (c >= p.I) break;
+      float av[2][4];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float g[4], u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          g[e] = acc[i][j][8 * q + e];
+          u[e] = acc[i][j][8 * q + 4 + e];
+          if (A) av[q][e] = glu_fwd(g[e], u[e], p.act, p.limit, p.alpha);
+        }
+        if (Z && c + 8 * q < p.I) {
+          *(float4*)z_block(p.z, row0, c + 8 * q, p.I, 0, lane) = make_float4(g[0], g[1], g[2], g[3]);
+          *(float4*)z_block(p.z, row0, c + 8 * q, p.I, 1, lane) = make_float4(u[0], u[1], u[2], u[3]);
+        }
+      }
+      if (A) {
+        const u32x4 v = pack_pair(av[0], av[1]);
+        const int cc = c + 8 * (lane >> 5);
+        if (row < p.T && cc < p.I) *(u32x4*)((uint16_t*)p.a + (size_t)row * p.I + cc) = v;
+      }
+    }
+  }
+}
+
+template <class C>
+__global__ __launch_bounds__(256, 1) void ffn_down_kernel(FfnArgs p) {
+  FFN_PROLOGUE(C)
+  KSrc<C::NBA> as;
+  KSrc<C::NBB> bs;
+  init_rows(as, p.a, m0, p.T, p.I, wave, lane);
+  init_rows(bs, p.wd, n0, p.H, p.I, wave, lane);
+  mainloop<C, bf16x8_t>(as, bs, p.I, lds, acc, wave, lane);
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+    const int row = m0 + wm * 32 * C::FM + 32 * i + (lane & 31), rc = min(row, p.T - 1);
+    const float s = row_gate(p.gate, rc);
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int c = n0 + (wn * C::FN + j) * 32 + 16 * q;
+        float v[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ch = c + 8 * h + 4 * (lane >> 5);
+          uint2 ad = make_uint2(0, 0);
+          if (p.add && ch < p.H) ad = *(const uint2*)((const uint16_t*)p.add + (size_t)rc * p.H + ch);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t w = e < 2 ? ad.x : ad.y;
+            v[h][e] = s * acc[i][j][8 * q + 4 * h + e] + __builtin_bit_cast(float, e & 1 ? w & 0xffff0000u : w << 16);
+          }
+        }
+        const u32x4 o = pack_pair(v[0], v[1]);
+        const int cc = c + 8 * (lane >> 5);
+        if (row < p.T && cc < p.H) *(u32x4*)((uint16_t*)p.out + (size_t)row * p.H + cc) = o;
+      }
+  }
+}
+
+template <class C, bool A, bool Z>
+hipError_t run_gate_up(const FfnArgs& p, hipStream_t s) {
+  const auto k = ffn_gate_up_kernel<C, A, Z>;
+  return run_kernel("ffn_gate_up", s, [&] { k<<<tile_grid(p.mt, p.nt), C::NT, 0, s>>>(p); });
+}
+
+}  // namespace dense
+
+using namespace dense;
+
+hipError_t launch_ffn_gate_up(FfnArgs p, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  with_tile(tile_kind(p.T, 2 * p.I, p.H), [&](auto c) {
+    using C = decltype(c);
+    p.mt = (p.T + C::BM - 1) / C::BM;
+    p.nt = (2 * p.I + C::BN - 1) / C::BN;
+    e = !p.z ? run_gate_up<C, true, false>(p, s) : p.a ? run_gate_up<C, true, true>(p, s) : run_gate_up<C, false, true>(p, s);
+  });
+  return e;
+}
+
+hipError_t launch_ffn_down(FfnArgs p, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  with_tile(tile_kind(p.T, p.H, p.I), [&](auto c) {
+    using C = decltype(c);
+    p.mt = (p.T + C::BM - 1) / C::BM;
+    p.nt = (p.H + C::BN - 1) / C::BN;
+    const auto k = ffn_down_kernel<C>;
+    e = run_kernel("ffn_down", s, [&] { k<<<tile_grid(p.mt, p.nt), C::NT, 0, s>>>(p); });
+  });
+  return e;
+}
+
+}  // namespace moe

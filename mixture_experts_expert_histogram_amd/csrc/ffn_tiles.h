@@ -1,0 +1,44 @@
+// Device pieces shared by the dense products of the feed-forward block.
+#pragma once
+#include "dense_tiles.h"
+#include "ffn.h"
+
+namespace moe {
+namespace dense {
+
+// Four fp32 values each of two 4-column groups (columns c .. and c + 8 .. of a
+// row, c = 4 (lane / 32)) as bf16, so that every lane ends with 8 consecutive
+// columns: lanes below 32 columns 0 .. 7, the others 8 .. 15 of the 16.
+__device__ __forceinline__ u32x4 pack_pair(const float* lo, const float* hi) {
+  const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16(lo[0], lo[1]), pack_bf16(hi[0], hi[1]), false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(pack_bf16(lo[2], lo[3]), pack_bf16(hi[2], hi[3]), false, false);
+  return u32x4{a[0], b[0], a[1], b[1]};
+}
+
+// Block of 32 rows x 8 columns of the saved gate (up = 0) and up values: 256
+// floats, lane l's four at 4 l, the order in which the accumulators hold them,
+// so that both passes move whole kilobytes.
+__device__ __forceinline__ float* z_block(float* z, int row, int col, int I, int up, int lane) {
+  return z + (((size_t)(row >> 5) * (I >> 3) + (col >> 3)) * 2 + up) * 256 + lane * 4;
+}
+
+__device__ __forceinline__ float row_gate(const float* gate, int row) { return gate ? 1.f / (1.f + expf(-gate[row])) : 1.f; }
+
+// A workgroup's tile, its wave's place in it and the results.
+#define FFN_PROLOGUE(C)                                                              \
+  __shared__ __align__(1024) char lds[C::NS * C::STAGE];                             \
+  int mt, nt;                                                                        \
+  if (!tile_of(blockIdx.x, p.mt, p.nt, mt, nt)) return;                              \
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); \
+  const int wm = wave >> 1, wn = wave & 1, m0 = mt * C::BM, n0 = nt * C::BN;         \
+  f32x16 acc[C::FM][C::FN];
+
+// Rows r0 .. of a matrix [rows][K] of bf16.
+template <class S>
+__device__ __forceinline__ void init_rows(S& s, const void* b, int r0, int rows, int K, int wave, int lane) {
+  s.init((const uint16_t*)b + (size_t)r0 * K, nullptr, [&](int r) { return (uint32_t)(min(r, rows - 1 - r0) * K * 2); }, wave,
+         lane);
+}
+
+}  // namespace dense
+}  // namespace moe

@@ -1,0 +1,375 @@
+// Newton-Schulz orthogonalisation of stacked matrices, and the optimiser step
+// around it:
+//
+//   m' = mu m + g,  u = g + mu m' (Nesterov) or m'   (a step; otherwise u = g)
+//   X = u / (|u| + eps)                                (2-norm of all elements)
+//   `steps` times:  P = X X^T,  Q = b P + c P P,  X <- a X + Q X
+//                   (matrices with more rows than columns: P = X^T X, X <- a X + X Q)
+//   w' = (1 - decay) w - lr X                          (a step; otherwise out = X)
+//
+// The products are bound by the matrix cores.  P and Q are symmetric, so only
+// their tiles on and above the diagonal are computed and the others are their
+// mirrors: 3 S^2 L + S^3 of 4 S^2 L + 2 S^3 operations a step (S the smaller, L
+// the larger side).  No operand is ever transposed in memory: the products
+// that contract over rows read their operands with transposing LDS reads.
+//
+// X, P and Q are held in fp16, which the singular values' known range allows
+// (at most 1.21 with the usual coefficients; the host checks others): 11
+// significant bits where bf16 has 8, at the same matrix rate.  With a bf16
+// result the whole is 2.1e-3 from 64 bits in the 2-norm, of which the result's
+// rounding is 1.66e-3; with bf16 iterates it would be 1.1e-2.  Factors 2^6 on X
+// and 2^12 on P and Q keep small elements out of the subnormal range.  Sums and
+// the polynomial's terms are fp32, the norm is summed in 64 bits (no overflow
+// or underflow of fp32 gradients' squares).
+#include "dense_tiles.h"
+#include "ortho.h"
+
+namespace moe {
+namespace dense {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const f16x2_t v = {(_Float16)lo, (_Float16)hi};
+  return __builtin_bit_cast(uint32_t, v);
+}
+// As pack_pair (ffn_tiles.h), to fp16.
+__device__ __forceinline__ u32x4 pack_pair_f16(const float* lo, const float* hi) {
+  const auto a = __builtin_amdgcn_permlane32_swap(pack_f16(lo[0], lo[1]), pack_f16(hi[0], hi[1]), false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(pack_f16(lo[2], lo[3]), pack_f16(hi[2], hi[3]), false, false);
+  return u32x4{a[0], b[0], a[1], b[1]};
+}
+
+// ------------------------------------------------------------------ norm and first iterate
+// 8 gradients (or updates) from element i on.
+template <bool F32>
+__device__ __forceinline__ void load8(const void* p, size_t i, float* v) {
+  if constexpr (F32) {
+    const float4 a = *(const float4*)((const float*)p + i), b = *(const float4*)((const float*)p + i + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 a = *(const uint4*)((const uint16_t*)p + i);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __builtin_bit_cast(float, e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+  }
+}
+
+// The update's squares, summed by workgroup, and a step's new momentum: one
+// pass over g (and m), bound by HBM.
+template <bool F32>
+__global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs p) {
+  __shared__ double red[4];
+  const size_t n = (size_t)p.M * p.N, at = n * blockIdx.y;
+  double sum = 0.0;
+  for (size_t i = (blockIdx.x * 256ul + threadIdx.x) * 8; i < n; i += gridDim.x * 2048ul) {
+    float u[8];
+    load8<F32>(p.g, at + i, u);
+    if (p.m) {
+      float m[8];
+      load8<true>(p.m, at + i, m);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        m[e] = p.momentum * m[e] + u[e];
+        u[e] = p.nesterov ? u[e] + p.momentum * m[e] : m[e];
+      }
+      *(float4*)(p.m_out + at + i) = make_float4(m[0], m[1], m[2], m[3]);
+      *(float4*)(p.m_out + at + i + 4) = make_float4(m[4], m[5], m[6], m[7]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += (double)u[e] * u[e];
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) p.part[blockIdx.y * ORTHO_PARTS + blockIdx.x] = red[0] + red[1] + red[2] + red[3];
+}
+
+// X = u / (|u| + eps) in fp16, times ORTHO_X; a step's u again from g and m'.
+template <bool F32>
+__global__ __launch_bounds__(256) void ortho_scale_kernel(OrthoArgs p, int parts) {
+  const size_t n = (size_t)p.M * p.N, at = n * blockIdx.y;
+  double sum = 0.0;
+  for (int i = 0; i < parts; ++i) sum += p.part[blockIdx.y * ORTHO_PARTS + i];
+  const float f = (float)(ORTHO_X / (sqrt(sum) + (double)p.eps));
+  for (size_t i = (blockIdx.x * 256ul + threadIdx.x) * 8; i < n; i += gridDim.x * 2048ul) {
+    float u[8];
+    load8<F32>(p.g, at + i, u);
+    if (p.m) {
+      float m[8];
+      load8<true>(p.m_out, at + i, m);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = p.nesterov ? u[e] + p.momentum * m[e] : m[e];
+    }
+    *(uint4*)((uint16_t*)p.x0 + at + i) = make_uint4(pack_f16(u[0] * f, u[1] * f), pack_f16(u[2] * f, u[3] * f),
+                                                    pack_f16(u[4] * f, u[5] * f), pack_f16(u[6] * f, u[7] * f));
+  }
+}
+
+// ------------------------------------------------------------------ symmetric products
+struct SymArgs {
+  const uint16_t* a;   // [E] matrices: rows of K (ROWS), or K rows of S
+  const uint16_t* p;   // QUAD: [E,S,S], the P of b P + c P P
+  uint16_t* out;       // [E,S,S]
+  size_t a_step;       // elements of a matrix of a
+  int E, S, K, tiles;  // tiles: of a side
+  float b, c;
+};
+
+// out = A A^T (QUAD: b P + c A A^T) for square tiles on and above the diagonal,
+// each stored where it belongs and, mirrored, below.  The mirror goes through
+// LDS: the tile is written there as it lies in the registers and read back with
+// the transposing reads.  COLS: A is held as its transpose (K rows of S).
+template <class C, bool COLS, bool QUAD>
+__global__ __launch_bounds__(256, 1) void ortho_sym_kernel(SymArgs p) {
+  static_assert(C::FM == C::FN && C::NS * C::STAGE >= 2 * C::BM * C::BN, "square tiles, held in the ring's LDS");
+  __shared__ __align__(1024) char lds[C::NS * C::STAGE];
+  const int per = p.tiles * (p.tiles + 1) / 2;
+  const int t = deal(blockIdx.x, per * p.E);
+  if (t < 0) return;
+  const int e = t / per;
+  int nt = t - e * per, mt = 0;   // row mt has tiles - mt tiles, from the diagonal on
+  while (nt >= p.tiles - mt) nt -= p.tiles - mt++;
+  nt += mt;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1, m0 = mt * C::BM, n0 = nt * C::BN, S = p.S, K = p.K;
+  f32x16 acc[C::FM][C::FN];
+  const uint16_t* A = p.a + p.a_step * e;
+  if constexpr (COLS) {
+    CSrc<C::NBA> as;
+    CSrc<C::NBB> bs;
+    as.init(A, S, m0, S, wave, lane);
+    bs.init(A, S, n0, S, wave, lane);
+    mainloop<C, f16x8_t>(as, bs, K, lds, acc, wave, lane);
+  } else {
+    KSrc<C::NBA> as;
+    KSrc<C::NBB> bs;
+    as.init(A + (size_t)m0 * K, nullptr, [&](int r) { return (uint32_t)(min(r, S - 1 - m0) * K * 2); }, wave, lane);
+    bs.init(A + (size_t)n0 * K, nullptr, [&](int r) { return (uint32_t)(min(r, S - 1 - n0) * K * 2); }, wave, lane);
+    mainloop<C, f16x8_t>(as, bs, K, lds, acc, wave, lane);
+  }
+  const uint16_t* P = p.p + (size_t)S * S * e;
+  uint16_t* out = p.out + (size_t)S * S * e;
+  // panels [BM rows][64 columns] of LDS, 16-byte chunks permuted as in FragSrc
+  const int r32 = lane & 31, x = (((r32 >> 1) & 1) << 2) | (((r32 >> 3) & 1) << 1);
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+    const int tr = wm * 32 * C::FM + 32 * i + r32, row = m0 + tr, rc = min(row, S - 1);
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int tc = (wn * C::FN + j) * 32 + 16 * q;
+        float v[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          f16x4_t pv = {0, 0, 0, 0};
+          const int c = n0 + tc + 8 * h + 4 * (lane >> 5);
+          if (QUAD && c < S) pv = *(const f16x4_t*)(P + (size_t)rc * S + c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float s = acc[i][j][8 * q + 4 * h + k];
+            v[h][k] = QUAD ? p.b * (float)pv[k] + p.c * s : s;
+          }
+          if (mt != nt) {
+            const int ct = tc + 8 * h;
+            *(uint2*)(lds + (ct >> 6) * (C::BM * 128) + tr * 128 + ((((ct >> 3) & 7) ^ x) << 4) + 8 * (lane >> 5)) =
+                make_uint2(pack_f16(v[h][0], v[h][1]), pack_f16(v[h][2], v[h][3]));
+          }
+        }
+        const u32x4 o = pack_pair_f16(v[0], v[1]);
+        const int cc = n0 + tc + 8 * (lane >> 5);
+        if (row < S && cc < S) *(u32x4*)(out + (size_t)row * S + cc) = o;
+      }
+  }
+  if (mt == nt) return;
+  __syncthreads();
+  // 32 columns x 16 rows a read: lane -> column lane % 32, rows 8 (lane / 32) .. + 7
+  const int g = lane >> 4, s4 = lane & 15, kr = ((g >> 1) << 3) + (s4 >> 2);
+  const int kx = (((kr >> 1) & 1) << 2) | (((kr >> 3) & 1) << 1);
+#pragma unroll 1
+  for (int cb = wave; cb < C::BN / 32; cb += 4) {
+    const int chunk = ((cb & 1) << 2) + ((g & 1) << 1) + ((s4 & 3) >> 1);
+    const lds_char* base = (const lds_char*)lds + (cb >> 1) * (C::BM * 128) + kr * 128 + ((chunk ^ kx) << 4) + (s4 & 1) * 8;
+    const int c = n0 + cb * 32 + r32;
+#pragma unroll
+    for (int k = 0; k < C::BM / 16; ++k) {
+      struct { s16x4_t h[2]; } v;
+      v.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + k * 2048));
+      v.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(base + k * 2048 + 512));
+      const int r = m0 + k * 16 + 8 * (lane >> 5);
+      if (c < S && r < S) *(u32x4*)(out + (size_t)c * S + r) = __builtin_bit_cast(u32x4, v);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ X <- a X + Q X (or X Q)
+enum { TO_X = 0, TO_BF16 = 1, TO_F32 = 2 };
+struct UpdateArgs {
+  const uint16_t *x, *q;
+  void* out;
+  const void* w;   // the weights that a step updates, or null
+  int E, M, N, S, mt, nt;
+  float a, lr, keep;
+};
+__device__ __forceinline__ void load4(const uint16_t* p, float* v) {
+  const uint2 w = *(const uint2*)p;
+  v[0] = __builtin_bit_cast(float, w.x << 16); v[1] = __builtin_bit_cast(float, w.x & 0xffff0000u);
+  v[2] = __builtin_bit_cast(float, w.y << 16); v[3] = __builtin_bit_cast(float, w.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const float4 w = *(const float4*)p;
+  v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+}
+
+template <class C, bool WIDE, int TO>
+__global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
+  using T = std::conditional_t<TO == TO_F32, float, uint16_t>;
+  __shared__ __align__(1024) char lds[C::NS * C::STAGE];
+  const int per = p.mt * p.nt, t = deal(blockIdx.x, per * p.E);
+  if (t < 0) return;
+  const int e = t / per;
+  int mt, nt;
+  tile_at(t - e * per, p.mt, p.nt, mt, nt);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1, m0 = mt * C::BM, n0 = nt * C::BN, M = p.M, N = p.N, S = p.S;
+  f32x16 acc[C::FM][C::FN];
+  const uint16_t *X = p.x + (size_t)M * N * e, *Q = p.q + (size_t)S * S * e;
+  const auto rows = [&](auto& src, const uint16_t* b, int r0, int n) {   // rows of S
+    src.init(b + (size_t)r0 * S, nullptr, [&](int r) { return (uint32_t)(min(r, n - 1 - r0) * S * 2); }, wave, lane);
+  };
+  KSrc<C::NBA> as;
+  if constexpr (WIDE) {
+    CSrc<C::NBB> bs;
+    rows(as, Q, m0, S);
+    bs.init(X, N, n0, N, wave, lane);
+    mainloop<C, f16x8_t>(as, bs, S, lds, acc, wave, lane);
+  } else {
+    KSrc<C::NBB> bs;
+    rows(as, X, m0, M);
+    rows(bs, Q, n0, S);
+    mainloop<C, f16x8_t>(as, bs, S, lds, acc, wave, lane);
+  }
+  // the products carry ORTHO_X ORTHO_P, x ORTHO_X
+  const float fx = TO == TO_X ? p.a : p.a / ORTHO_X, fs = TO == TO_X ? 1.f / ORTHO_P : 1.f / (ORTHO_X * ORTHO_P);
+  const size_t at = (size_t)M * N * e;
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+    const int row = m0 + wm * 32 * C::FM + 32 * i + (lane & 31), rc = min(row, M - 1);
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int c = n0 + (wn * C::FN + j) * 32 + 16 * q;
+        float v[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int ch = min(c + 8 * h, N - 8) + 4 * (lane >> 5);
+          const f16x4_t xv = *(const f16x4_t*)(X + (size_t)rc * N + ch);
+          float w[4] = {0.f, 0.f, 0.f, 0.f};
+          if (TO != TO_X && p.w) load4((const T*)p.w + at + (size_t)rc * N + ch, w);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float o = fx * (float)xv[k] + fs * acc[i][j][8 * q + 4 * h + k];
+            v[h][k] = TO != TO_X && p.w ? p.keep * w[k] - p.lr * o : o;
+          }
+        }
+        if constexpr (TO == TO_F32) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int ch = c + 8 * h + 4 * (lane >> 5);
+            if (row < M && ch < N) store4<float>((float*)p.out + at + (size_t)row * N + ch, v[h][0], v[h][1], v[h][2], v[h][3]);
+          }
+        } else {
+          u32x4 o;
+          if constexpr (TO == TO_X) {
+            o = pack_pair_f16(v[0], v[1]);
+          } else {
+            const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16(v[0][0], v[0][1]), pack_bf16(v[1][0], v[1][1]), false, false);
+            const auto b = __builtin_amdgcn_permlane32_swap(pack_bf16(v[0][2], v[0][3]), pack_bf16(v[1][2], v[1][3]), false, false);
+            o = u32x4{a[0], b[0], a[1], b[1]};
+          }
+          const int cc = c + 8 * (lane >> 5);
+          if (row < M && cc < N) *(u32x4*)((uint16_t*)p.out + at + (size_t)row * N + cc) = o;
+        }
+      }
+  }
+}
+
+// ------------------------------------------------------------------ host
+template <class C, bool COLS, bool QUAD>
+hipError_t run_sym(const SymArgs& p, hipStream_t s) {
+  const auto k = ortho_sym_kernel<C, COLS, QUAD>;
+  const long tiles = (long)p.E * p.tiles * (p.tiles + 1) / 2;
+  return run_kernel(QUAD ? "ortho_quad" : "ortho_gram", s, [&] { k<<<deal_grid(tiles), C::NT, 0, s>>>(p); });
+}
+// Square tiles only.
+hipError_t sym(SymArgs p, bool cols, bool quad, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  with_square_tile(square_tile_kind(p.S, p.K, p.E), [&](auto c) {
+    using C = decltype(c);
+    p.tiles = (p.S + C::BM - 1) / C::BM;
+    e = quad ? run_sym<C, false, true>(p, s) : cols ? run_sym<C, true, false>(p, s) : run_sym<C, false, false>(p, s);
+  });
+  return e;
+}
+
+template <class C, bool WIDE, int TO>
+hipError_t run_update(const UpdateArgs& p, hipStream_t s) {
+  const auto k = ortho_update_kernel<C, WIDE, TO>;
+  return run_kernel("ortho_update", s, [&] { k<<<deal_grid((long)p.E * p.mt * p.nt), C::NT, 0, s>>>(p); });
+}
+hipError_t update(UpdateArgs p, int to, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  with_tile(tile_kind(p.M, p.N, p.S, p.E), [&](auto c) {
+    using C = decltype(c);
+    p.mt = (p.M + C::BM - 1) / C::BM;
+    p.nt = (p.N + C::BN - 1) / C::BN;
+    const auto run = [&](auto wide) {
+      constexpr bool W = decltype(wide)::value;
+      return to == TO_X ? run_update<C, W, TO_X>(p, s) : to == TO_BF16 ? run_update<C, W, TO_BF16>(p, s) : run_update<C, W, TO_F32>(p, s);
+    };
+    e = p.M <= p.N ? run(std::true_type{}) : run(std::false_type{});
+  });
+  return e;
+}
+
+}  // namespace dense
+
+using namespace dense;
+
+hipError_t launch_ortho(const OrthoArgs& p, hipStream_t s) {
+  const size_t n = (size_t)p.M * p.N;
+  const size_t want = (n + 8191) / 8192;   // 4 groups of 8 elements a thread, or more
+  const int parts = (int)(want < ORTHO_PARTS ? want : ORTHO_PARTS);
+  hipError_t e = run_kernel("ortho_norm", s, [&] {
+    if (p.g_f32) ortho_norm_kernel<true><<<dim3(parts, p.E), 256, 0, s>>>(p);
+    else ortho_norm_kernel<false><<<dim3(parts, p.E), 256, 0, s>>>(p);
+  });
+  if (e != hipSuccess) return e;
+  e = run_kernel("ortho_scale", s, [&] {
+    if (p.g_f32) ortho_scale_kernel<true><<<dim3(parts, p.E), 256, 0, s>>>(p, parts);
+    else ortho_scale_kernel<false><<<dim3(parts, p.E), 256, 0, s>>>(p, parts);
+  });
+  const bool wide = p.M <= p.N;
+  uint16_t *x = (uint16_t*)p.x0, *y = (uint16_t*)p.x1, *P = (uint16_t*)p.p, *Q = (uint16_t*)p.q;
+  const size_t ss = (size_t)p.S * p.S;
+  for (int i = 0; i < p.steps && e == hipSuccess; ++i) {
+    const bool last = i + 1 == p.steps;
+    // X X^T carries ORTHO_X^2 = ORTHO_P; P P carries ORTHO_P^2
+    e = sym({x, nullptr, P, n, p.E, p.S, wide ? p.N : p.M, 0, 0.f, 1.f}, !wide, false, s);
+    if (e == hipSuccess) e = sym({P, P, Q, ss, p.E, p.S, p.S, 0, p.b, p.c / ORTHO_P}, false, true, s);
+    if (e == hipSuccess)
+      e = update({x, Q, last ? p.out : y, last ? p.w : nullptr, p.E, p.M, p.N, p.S, 0, 0, p.a, p.lr, p.keep},
+                 !last ? TO_X : p.out_f32 ? TO_F32 : TO_BF16, s);
+    uint16_t* t = x;
+    x = y;
+    y = t;
+  }
+  return e;
+}
+
+}  // namespace moe

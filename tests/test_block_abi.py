@@ -1,0 +1,141 @@
+"""Refusals of the operators around the routed experts, before any launch (no GPU is touched)."""
+import ctypes
+
+import pytest
+import torch
+
+import mixture_experts_expert_histogram_amd as moe
+from mixture_experts_expert_histogram_amd import _lib
+from mixture_experts_expert_histogram_amd._lib import Muon, NormDesc, OrthoDesc
+
+P = ctypes.c_void_p(16)
+BIG = 1 << 45
+
+
+def call(f, desc, order, over, ws_bytes=BIG, saved_bytes=BIG):
+    args = []
+    for n in order.split():
+        args.append({"SB": saved_bytes, "WB": ws_bytes}[n] if n in ("SB", "WB") else over.get(n, P))
+    return getattr(moe.library(), f)(ctypes.byref(desc) if desc is not None else None, *args, None)
+
+
+FFN_FWD = ("moe_ffn_fwd", "x gu dn gate add out saved SB ws WB", "x gu dn out ws")
+FFN_BWD = ("moe_ffn_bwd", "x gu dn gate dout saved SB dx dgate dgu ddn ws WB", "x gu dn dout dx dgate dgu ddn ws")
+NORM_FWD = ("moe_norm_fwd", "x w y", "x w y")
+NORM_BWD = ("moe_norm_bwd", "x w dy dadd dx dw ws WB", "x w dy dx dw ws")
+RES_FWD = ("moe_residual_fwd", "x h post gate next new y", "x h gate new y")
+RES_BWD = ("moe_residual_bwd", "new h post gate next dnew dy dx dh dgate dpost dnext ws WB", "new h gate dy dx dh dgate dpost dnext ws")
+ORTHO = ("moe_orthogonalize", "g out ws WB", "g out ws")
+
+
+def ffn_desc(T=8, H=64, I=32, E=1, K=1, dtype="bf16"):
+    return moe.make_desc(T, H, I, E, K, dtype)
+
+
+def norm_desc(T=8, H=64, dtype=0, kind=0, scale=1.0, eps=1e-5):
+    return NormDesc(T, H, dtype, kind, scale, eps)
+
+
+def ortho_desc(E=2, M=64, N=32, dtype=0, out=0, steps=5, coef=moe.NEWTON_SCHULZ, eps=1e-7):
+    return OrthoDesc(E, M, N, dtype, out, steps, *coef, eps)
+
+
+@pytest.mark.parametrize("entry,desc", [(FFN_FWD, ffn_desc()), (FFN_BWD, ffn_desc()), (NORM_FWD, norm_desc()), (NORM_BWD, norm_desc()),
+                                        (RES_FWD, norm_desc(kind=1)), (RES_BWD, norm_desc(kind=1)), (ORTHO, ortho_desc())])
+def test_pointers(entry, desc):
+    f, order, required = entry
+    for n in required.split():
+        assert call(f, desc, order, {n: None}) == _lib.MOE_ERR_INVALID_ARG, n
+    for n in order.split():
+        if n not in ("SB", "WB"):
+            assert call(f, desc, order, {n: ctypes.c_void_p(24)}) == _lib.MOE_ERR_INVALID_ARG, n
+    assert call(f, None, order, {}) == _lib.MOE_ERR_INVALID_ARG
+    if "WB" in order:
+        assert call(f, desc, order, {}, ws_bytes=255) == _lib.MOE_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("entry", [FFN_FWD, FFN_BWD])
+def test_ffn_limits(entry):
+    f, order, _ = entry
+    for bad in (ffn_desc(E=2), ffn_desc(E=2, K=2), ffn_desc(T=-1)):
+        assert call(f, bad, order, {}) == _lib.MOE_ERR_INVALID_ARG
+    for big in (ffn_desc(H=60), ffn_desc(I=12), ffn_desc(H=1 << 21), ffn_desc(H=1 << 15, I=1 << 14), ffn_desc(T=1 << 31)):
+        assert call(f, big, order, {}) == _lib.MOE_ERR_UNSUPPORTED
+    d = ffn_desc(T=100)
+    assert call(f, d, order, {}, saved_bytes=8) == _lib.MOE_ERR_WORKSPACE
+    for dtype in ("bf16", "fp32"):
+        d = ffn_desc(T=100, dtype=dtype)
+        fws, bws, _ = moe.ffn_workspace_size(d)
+        assert call(f, d, order, {}, ws_bytes=(fws if entry is FFN_FWD else bws) - 1) == _lib.MOE_ERR_WORKSPACE
+    d.act = 7
+    assert call(f, d, order, {}) == _lib.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("entry", [NORM_FWD, NORM_BWD, RES_FWD, RES_BWD])
+def test_norm_limits(entry):
+    f, order, _ = entry
+    kind = 1 if "residual" in f else 0
+    for bad in (norm_desc(T=-1, kind=kind), norm_desc(H=0, kind=kind), norm_desc(dtype=2, kind=kind), norm_desc(kind=4),
+                norm_desc(kind=-1), norm_desc(eps=-1.0, kind=kind), norm_desc(eps=float("nan"), kind=kind), norm_desc(kind=1 - kind)):
+        assert call(f, bad, order, {}) == _lib.MOE_ERR_INVALID_ARG
+    for big in (norm_desc(H=60, kind=kind), norm_desc(H=16392, kind=kind), norm_desc(T=1 << 31, kind=kind)):
+        assert call(f, big, order, {}) == _lib.MOE_ERR_UNSUPPORTED
+    if kind:
+        assert call(f, norm_desc(kind=0), order, {}) == _lib.MOE_ERR_INVALID_ARG   # a gate without a kind
+    assert moe.norm_workspace_size(norm_desc(T=10 ** 6, H=4096)) <= 3 * 512 * 4096 * 4
+
+
+def test_ortho_limits():
+    f, order, _ = ORTHO
+    for bad in (ortho_desc(E=-1), ortho_desc(M=0), ortho_desc(N=-8), ortho_desc(dtype=2), ortho_desc(out=-1), ortho_desc(eps=-1.0),
+                ortho_desc(eps=float("nan"))):
+        assert call(f, bad, order, {}) == _lib.MOE_ERR_INVALID_ARG
+    nan = float("nan")
+    for big in (ortho_desc(M=60), ortho_desc(N=12), ortho_desc(E=65536), ortho_desc(steps=0), ortho_desc(steps=65),
+                ortho_desc(M=1 << 21), ortho_desc(coef=(10.0, 0.0, 0.0)), ortho_desc(coef=(3.5, -20.0, 3.0)),
+                ortho_desc(coef=(nan, 0.0, 0.0)), ortho_desc(coef=(1.0, float("inf"), 0.0))):
+        assert call(f, big, order, {}) == _lib.MOE_ERR_UNSUPPORTED
+    n = moe.ortho_workspace_size(ortho_desc())
+    assert call(f, ortho_desc(), order, {}, ws_bytes=n - 1) == _lib.MOE_ERR_WORKSPACE
+    # a polynomial that grows is fine while it stays within the range
+    assert moe.ortho_workspace_size(ortho_desc(steps=1, coef=(10.0, 0.0, 0.0))) > 0
+    assert call(f, ortho_desc(E=0), order, {"g": None, "out": None, "ws": None}, ws_bytes=0) == _lib.MOE_OK
+
+
+def test_muon_arguments():
+    lib, d = moe.library(), ortho_desc()
+    names = ("w", "g", "m", "w_out", "m_out", "ws")
+
+    def step(opt=Muon(0.1, 0.9, 0.0, 1), ws_bytes=BIG, **over):
+        return lib.moe_muon_step(ctypes.byref(d), ctypes.byref(opt) if opt else None, *[over.get(n, P) for n in names], ws_bytes, None)
+    for n in names:
+        assert step(**{n: None}) == _lib.MOE_ERR_INVALID_ARG
+        assert step(**{n: ctypes.c_void_p(8)}) == _lib.MOE_ERR_INVALID_ARG
+    assert step(opt=None) == _lib.MOE_ERR_INVALID_ARG
+    assert step(opt=Muon(0.1, 0.9, 0.0, 2)) == _lib.MOE_ERR_INVALID_ARG
+    assert step(ws_bytes=1) == _lib.MOE_ERR_WORKSPACE
+
+
+def test_size_queries_need_a_place():
+    lib = moe.library()
+    assert lib.moe_norm_workspace_size(ctypes.byref(norm_desc()), None) == _lib.MOE_ERR_INVALID_ARG
+    assert lib.moe_ortho_workspace_size(ctypes.byref(ortho_desc()), None) == _lib.MOE_ERR_INVALID_ARG
+    assert lib.moe_ffn_workspace_size(ctypes.byref(ffn_desc()), None, None, None) == _lib.MOE_OK
+
+
+def test_nothing_to_do_launches_nothing():
+    f, order, _ = FFN_FWD
+    assert call(f, ffn_desc(T=0), order, {"x": None, "out": None}) == _lib.MOE_OK
+    assert call(NORM_FWD[0], norm_desc(T=0), NORM_FWD[1], {"x": None, "y": None}) == _lib.MOE_OK
+    assert call(RES_FWD[0], norm_desc(T=0, kind=1), RES_FWD[1], {"x": None, "h": None, "new": None, "y": None}) == _lib.MOE_OK
+
+
+def test_binding_refuses_host_and_odd_tensors():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    gu, dn = torch.zeros(64, 64, dtype=torch.bfloat16), torch.zeros(64, 32, dtype=torch.bfloat16)
+    for f in (lambda: moe.ffn_fwd(x, gu, dn), lambda: moe.ffn_bwd(x, gu, dn, x), lambda: moe.norm_fwd(x, x[0]),
+              lambda: moe.norm_bwd(x, x[0], x), lambda: moe.residual_fwd(x, x), lambda: moe.residual_bwd(x, x),
+              lambda: moe.residual_fwd(x, x, gate=x[:, :2]), lambda: moe.orthogonalize(gu), lambda: moe.muon_step(gu, gu, gu.float(), 0.1),
+              lambda: moe.orthogonalize(gu, dtype="fp16"), lambda: moe.ffn_fwd(x, gu, dn, act="relu")):
+        with pytest.raises(ValueError):
+            f()
