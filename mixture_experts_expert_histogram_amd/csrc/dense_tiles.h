@@ -8,31 +8,40 @@ namespace moe {
 namespace dense {
 
 // ------------------------------------------------------------------ tiles
-// Kernels exist for these tiles (rows x columns / 64, stages).  Time of a step
-// of 64 k and of a tile's start and end in us, as timed with 256 workgroups
-// that fill the card (T11 and T22: two a CU, so per pair of them).
+// Kernels exist for these tiles (rows x columns / 64).  Times in us of a step
+// of 64 k with one workgroup a CU and with per_cu of them, and of a tile's
+// start and end, from products that fill the card's rounds (8192 x 4096 x 8192:
+// 398 us on 256 x 256 tiles, 455 on 256 x 192; 4096 x 2880 x 5760: 130 and 110;
+// 5760 x 2880 x 4096: 185 on 256 x 256, 135 on 192 x 192; 512 x 4096 x 4096: 27
+// on 128 x 128, 24 on 128 x 64, 26 on 64 x 64; 130 x 4096 x 4096: 24, 20, 13).
 struct TileKind {
-  int fm, fn, stages, per_cu;
-  float step, ends;
+  int fm, fn, per_cu;
+  float solo, full, ends;
 };
 constexpr TileKind kTiles[] = {
-    {4, 4, 2, 1, 1.77f, 8.f}, {4, 3, 2, 1, 1.25f, 7.f}, {3, 3, 3, 1, 0.92f, 6.f}, {2, 2, 2, 2, 0.96f, 5.f}, {1, 1, 4, 2, 0.38f, 4.f},
+    {4, 4, 1, 1.50f, 1.50f, 8.f}, {4, 3, 1, 1.17f, 1.17f, 7.f}, {3, 3, 1, 0.92f, 0.92f, 6.f},
+    {2, 2, 1, 0.45f, 0.45f, 4.f}, {2, 1, 2, 0.31f, 0.57f, 4.f}, {1, 1, 2, 0.155f, 0.34f, 3.5f},
 };
-constexpr int N_TILES = 5;
+constexpr int N_TILES = 6;
+
+// Time of `tiles` tiles of a kind over K: rounds of 256 CUs; fewer workgroups
+// than CUs each run faster (clocks and memory are shared by fewer: 144 tiles of
+// 256 x 256 took 0.83 of a round's time, 64 of 128 x 128 0.73).
+inline float tile_time(const TileKind& k, long tiles, long K) {
+  const float nk = (float)((K + 63) / 64);
+  if (tiles <= 256) return (nk * k.solo + k.ends) * (0.65f + 0.35f * (float)tiles / 256.f);
+  const long slots = 256 * k.per_cu;
+  return (float)((tiles + slots - 1) / slots) * (nk * k.full + k.ends);
+}
 
 // The kind of tile that an M x N product over K, `batch` times, is done with
-// soonest: rounds of workgroups over 256 CUs times the time of one.
+// soonest.
 inline int tile_kind(long M, long N, long K, long batch = 1) {
   int best = 0;
   float least = 0.f;
   for (int i = 0; i < N_TILES; ++i) {
     const TileKind& k = kTiles[i];
-    const long tiles = batch * ((M + 64 * k.fm - 1) / (64 * k.fm)) * ((N + 64 * k.fn - 1) / (64 * k.fn));
-    const float nk = (float)((K + 63) / 64);
-    // a CU with one of the small tiles takes about half a pair's time
-    const long slots = 256 * k.per_cu;
-    const float one = k.per_cu == 2 && tiles <= 256 ? 0.5f : 1.f;
-    const float t = (float)((tiles + slots - 1) / slots) * (nk * k.step * one + k.ends);
+    const float t = tile_time(k, batch * ((M + 64 * k.fm - 1) / (64 * k.fm)) * ((N + 64 * k.fn - 1) / (64 * k.fn)), K);
     if (i == 0 || t < least) best = i, least = t;
   }
   return best;
@@ -42,11 +51,12 @@ inline int tile_kind(long M, long N, long K, long batch = 1) {
 template <class F>
 inline void with_tile(int kind, F launch) {
   switch (kind) {
-    case 0: return launch(Cfg<4, 4, 2>{});
-    case 1: return launch(Cfg<4, 3, 2>{});
-    case 2: return launch(Cfg<3, 3, 3>{});
-    case 3: return launch(Cfg<2, 2, 2>{});
-    default: return launch(Cfg<1, 1, 4>{});
+    case 0: return launch(Cfg<4, 4, 3, 2>{});
+    case 1: return launch(Cfg<4, 3, 3, 2>{});
+    case 2: return launch(Cfg<3, 3, 3, 3>{});
+    case 3: return launch(Cfg<2, 2, 3, 3>{});
+    case 4: return launch(Cfg<2, 1, 3, 3>{});
+    default: return launch(Cfg<1, 1, 5, 5>{});
   }
 }
 
@@ -58,9 +68,8 @@ inline int square_tile_kind(long S, long K, long batch) {
   for (int i = 0; i < N_TILES; ++i) {
     const TileKind& k = kTiles[i];
     if (k.fm != k.fn) continue;
-    const long side = (S + 64 * k.fm - 1) / (64 * k.fm), tiles = batch * side * (side + 1) / 2, slots = 256 * k.per_cu;
-    const float one = k.per_cu == 2 && tiles <= 256 ? 0.5f : 1.f;
-    const float t = (float)((tiles + slots - 1) / slots) * ((float)((K + 63) / 64) * k.step * one + k.ends);
+    const long side = (S + 64 * k.fm - 1) / (64 * k.fm);
+    const float t = tile_time(k, batch * side * (side + 1) / 2, K);
     if (best < 0 || t < least) best = i, least = t;
   }
   return best;
@@ -68,10 +77,10 @@ inline int square_tile_kind(long S, long K, long batch) {
 template <class F>
 inline void with_square_tile(int kind, F launch) {
   switch (kind) {
-    case 0: return launch(Cfg<4, 4, 2>{});
-    case 2: return launch(Cfg<3, 3, 3>{});
-    case 3: return launch(Cfg<2, 2, 2>{});
-    default: return launch(Cfg<1, 1, 4>{});
+    case 0: return launch(Cfg<4, 4, 3, 2>{});
+    case 2: return launch(Cfg<3, 3, 3, 3>{});
+    case 3: return launch(Cfg<2, 2, 3, 3>{});
+    default: return launch(Cfg<1, 1, 5, 5>{});
   }
 }
 

@@ -26,7 +26,7 @@ __device__ __forceinline__ float row_gate(const float* gate, int row) { return g
 
 // A workgroup's tile, its wave's place in it and the results.
 #define FFN_PROLOGUE(C)                                                              \
-  __shared__ __align__(1024) char lds[C::NS * C::STAGE];                             \
+  __shared__ __align__(1024) char lds[C::LDS];                             \
   int mt, nt;                                                                        \
   if (!tile_of(blockIdx.x, p.mt, p.nt, mt, nt)) return;                              \
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); \

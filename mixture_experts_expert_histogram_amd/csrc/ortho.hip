@@ -125,8 +125,8 @@ struct SymArgs {
 // the transposing reads.  COLS: A is held as its transpose (K rows of S).
 template <class C, bool COLS, bool QUAD>
 __global__ __launch_bounds__(256, 1) void ortho_sym_kernel(SymArgs p) {
-  static_assert(C::FM == C::FN && C::NS * C::STAGE >= 2 * C::BM * C::BN, "square tiles, held in the ring's LDS");
-  __shared__ __align__(1024) char lds[C::NS * C::STAGE];
+  static_assert(C::FM == C::FN && C::LDS >= 2 * C::BM * C::BN, "square tiles, held in the ring's LDS");
+  __shared__ __align__(1024) char lds[C::LDS];
   const int per = p.tiles * (p.tiles + 1) / 2;
   const int t = deal(blockIdx.x, per * p.E);
   if (t < 0) return;
@@ -228,7 +228,7 @@ __device__ __forceinline__ void load4(const float* p, float* v) {
 template <class C, bool WIDE, int TO>
 __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
   using T = std::conditional_t<TO == TO_F32, float, uint16_t>;
-  __shared__ __align__(1024) char lds[C::NS * C::STAGE];
+  __shared__ __align__(1024) char lds[C::LDS];
   const int per = p.mt * p.nt, t = deal(blockIdx.x, per * p.E);
   if (t < 0) return;
   const int e = t / per;
