@@ -1,11 +1,33 @@
 // The choice of the dense products' tiles, and their launches.
 #pragma once
 #include <type_traits>
+#include <utility>
 
 #include "dense.h"
 
 namespace moe {
 namespace dense {
+
+// A wave's FM x FN result fragments in turn, use(i, j, r) with what fetch(i, j,
+// r) loaded for each DEPTH fragments earlier, so that an epilogue waits for
+// memory once and not once a fragment.
+template <class C, class R, int D, class Fetch, class Use, int... F>
+__device__ __forceinline__ void each_fragment_of(Fetch fetch, Use use, std::integer_sequence<int, F...>) {
+  R ring[D];
+#pragma unroll
+  for (int f = 0; f < D; ++f) fetch(f / C::FN, f % C::FN, ring[f]);
+  __builtin_amdgcn_sched_barrier(0);
+  ([&]() __attribute__((always_inline)) {   // not a loop: every index into the results has to be a constant
+    use(F / C::FN, F % C::FN, ring[F % D]);
+    if constexpr (F + D < (int)sizeof...(F)) fetch((F + D) / C::FN, (F + D) % C::FN, ring[F % D]);
+    __builtin_amdgcn_sched_barrier(0);
+  }(), ...);
+}
+template <class C, class R, int DEPTH, class Fetch, class Use>
+__device__ __forceinline__ void each_fragment(Fetch fetch, Use use) {
+  constexpr int N = C::FM * C::FN;
+  each_fragment_of<C, R, (DEPTH < N ? DEPTH : N)>(fetch, use, std::make_integer_sequence<int, N>{});
+}
 
 // ------------------------------------------------------------------ tiles
 // Kernels exist for these tiles (rows x columns / 64).  Times in us of a step

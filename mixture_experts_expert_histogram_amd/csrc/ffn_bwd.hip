@@ -11,7 +11,8 @@
 namespace moe {
 namespace dense {
 
-template <class C>
+// ACT: 0 swiglu, 1 clamped
+template <class C, int ACT>
 __global__ __launch_bounds__(256, 1) void ffn_down_dgrad_kernel(FfnArgs p) {
   FFN_PROLOGUE(C)
   KSrc<C::NBA> as;
@@ -20,63 +21,71 @@ __global__ __launch_bounds__(256, 1) void ffn_down_dgrad_kernel(FfnArgs p) {
   bs.init(p.wd, p.I, n0, p.I, wave, lane);
   mainloop<C, bf16x8_t>(as, bs, p.H, lds, acc, wave, lane);
   const int I = p.I;
+  const int r0 = m0 + wm * 32 * C::FM, r32 = lane & 31, c00 = n0 + wn * 32 * C::FN;
+  float s[C::FM], sum[C::FM];
 #pragma unroll
   for (int i = 0; i < C::FM; ++i) {
-    const int row0 = m0 + wm * 32 * C::FM + 32 * i, row = row0 + (lane & 31);
-    if (row0 >= p.T) break;
-    const float s = row_gate(p.gate, min(row, p.T - 1));
-    float sum = 0.f;
+    s[i] = row_gate(p.gate, min(r0 + 32 * i + r32, p.T - 1));
+    sum[i] = 0.f;
+  }
+  // The fragment's gate and up values; blocks of rows or columns past the last
+  // read the last one (what comes of it is not stored).
+  struct Z { float4 g[4], u[4]; };
+  const int last = ((p.T - 1) >> 5) << 5;
+  each_fragment<C, Z, 2>(
+      [&](int i, int j, Z& z) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) {
-      const int c0 = n0 + (wn * C::FN + j) * 32;
-      if (c0 >= I) break;
-      float4 zg[4], zu[4];   // the fragment's values, loaded together; groups past I read the last one
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int c = min(c0 + 8 * v, I - 8);
-        zg[v] = *(const float4*)z_block(p.z, row0, c, I, 0, lane);
-        zu[v] = *(const float4*)z_block(p.z, row0, c, I, 1, lane);
-      }
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float dg[2][4], du[2][4], a[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 g4 = zg[2 * q + h], u4 = zu[2 * q + h];
-          const float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
-          const bool ok = c0 + 16 * q + 8 * h < I;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float r = acc[i][j][8 * q + 4 * h + e];
-            const float v = glu_bwd(g[e], u[e], s * r, p.act, p.limit, p.alpha, dg[h][e], du[h][e]);
-            if (ok) sum += r * v;
-            a[h][e] = s * v;
-          }
+        for (int v = 0; v < 4; ++v) {
+          const int c = min(c00 + 32 * j + 8 * v, I - 8);
+          z.g[v] = *(const float4*)z_block(p.z, min(r0 + 32 * i, last), c, I, 0, lane);
+          z.u[v] = *(const float4*)z_block(p.z, min(r0 + 32 * i, last), c, I, 1, lane);
         }
-        const u32x4 av = pack_pair(a[0], a[1]);
-        const int cc = c0 + 16 * q + 8 * (lane >> 5);
-        const bool ok = row < p.T && cc < I;
-        if (ok) *(u32x4*)((uint16_t*)p.aw + (size_t)row * I + cc) = av;
-        uint16_t* dz = (uint16_t*)p.dz + (size_t)row * 2 * I;
-        if (p.layout) {
+      },
+      [&](int i, int j, const Z& z) __attribute__((always_inline)) {
+        const int row = r0 + 32 * i + r32, c0 = c00 + 32 * j;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float dg[2][4], du[2][4], a[2][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int ch = c0 + 16 * q + 8 * h + 4 * (lane >> 5);
-            if (row < p.T && ch < I) store4x2<uint16_t>(dz + 2 * ch, dg[h], du[h]);
+            const float4 g4 = z.g[2 * q + h], u4 = z.u[2 * q + h];
+            const float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
+            float rv = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float r = acc[i][j][8 * q + 4 * h + e];
+              const float v = glu_bwd_t<ACT>(g[e], u[e], s[i] * r, p.limit, p.alpha, dg[h][e], du[h][e]);
+              rv += r * v;
+              a[h][e] = s[i] * v;
+            }
+            if (c0 + 16 * q + 8 * h < I) sum[i] += rv;
           }
-        } else {
-          const u32x4 gv = pack_pair(dg[0], dg[1]), uv = pack_pair(du[0], du[1]);
-          if (ok) {
-            *(u32x4*)(dz + cc) = gv;
-            *(u32x4*)(dz + I + cc) = uv;
+          const u32x4 av = pack_pair(a[0], a[1]);
+          const int cc = c0 + 16 * q + 8 * (lane >> 5);
+          const bool ok = row < p.T && cc < I;
+          if (ok) *(u32x4*)((uint16_t*)p.aw + (size_t)row * I + cc) = av;
+          uint16_t* dz = (uint16_t*)p.dz + (size_t)row * 2 * I;
+          if (p.layout) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int ch = c0 + 16 * q + 8 * h + 4 * (lane >> 5);
+              if (row < p.T && ch < I) store4x2<uint16_t>(dz + 2 * ch, dg[h], du[h]);
+            }
+          } else {
+            const u32x4 gv = pack_pair(dg[0], dg[1]), uv = pack_pair(du[0], du[1]);
+            if (ok) {
+              *(u32x4*)(dz + cc) = gv;
+              *(u32x4*)(dz + I + cc) = uv;
+            }
           }
         }
-      }
-    }
-    if (p.dgate) {
-      sum += __shfl_xor(sum, 32);   // the other half of the row's columns
-      if (lane < 32 && row < p.T) p.part[(size_t)row * p.parts + nt * 2 + wn] = sum;
-    }
+      });
+  if (!p.dgate) return;
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+    const int row = r0 + 32 * i + r32;
+    sum[i] += __shfl_xor(sum[i], 32);   // the other half of the row's columns
+    if (lane < 32 && row < p.T) p.part[(size_t)row * p.parts + nt * 2 + wn] = sum[i];
   }
 }
 
@@ -183,7 +192,7 @@ hipError_t launch_ffn_down_dgrad(FfnArgs p, hipStream_t s) {
     p.mt = (p.T + C::BM - 1) / C::BM;
     p.nt = (p.I + C::BN - 1) / C::BN;
     p.parts = 2 * p.nt;
-    const auto k = ffn_down_dgrad_kernel<C>;
+    const auto k = p.act ? ffn_down_dgrad_kernel<C, 1> : ffn_down_dgrad_kernel<C, 0>;
     e = run_kernel("ffn_down_dgrad", s, [&] { k<<<tile_grid(p.mt, p.nt), C::NT, 0, s>>>(p); });
   });
   if (e != hipSuccess || !p.dgate) return e;

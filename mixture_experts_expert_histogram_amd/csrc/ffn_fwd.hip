@@ -13,7 +13,8 @@ namespace dense {
 // Tile rows of B take gate and up rows in turns of 8, so that accumulator
 // groups v / 4 = 0, 2 are gate and 1, 3 up values of the same 8 columns and phi
 // needs no exchange between lanes.
-template <class C, bool A, bool Z>
+// ACT: 0 swiglu, 1 clamped; A, Z: which results are written
+template <class C, int ACT, bool A, bool Z>
 __global__ __launch_bounds__(256, 1) void ffn_gate_up_kernel(FfnArgs p) {
   FFN_PROLOGUE(C)
   const int j0 = nt * (C::BN / 2);
@@ -40,7 +41,7 @@ __global__ __launch_bounds__(256, 1) void ffn_gate_up_kernel(FfnArgs p) {
         for (int e = 0; e < 4; ++e) {
           g[e] = acc[i][j][8 * q + e];
           u[e] = acc[i][j][8 * q + 4 + e];
-          if (A) av[q][e] = glu_fwd(g[e], u[e], p.act, p.limit, p.alpha);
+          if (A) av[q][e] = glu_fwd_t<ACT>(g[e], u[e], p.limit, p.alpha);
         }
         if (Z && c + 8 * q < p.I) {
           *(float4*)z_block(p.z, row0, c + 8 * q, p.I, 0, lane) = make_float4(g[0], g[1], g[2], g[3]);
@@ -64,37 +65,41 @@ __global__ __launch_bounds__(256, 1) void ffn_down_kernel(FfnArgs p) {
   init_rows(as, p.a, m0, p.T, p.I, wave, lane);
   init_rows(bs, p.wd, n0, p.H, p.I, wave, lane);
   mainloop<C, bf16x8_t>(as, bs, p.I, lds, acc, wave, lane);
+  const int r0 = m0 + wm * 32 * C::FM + (lane & 31), c00 = n0 + wn * 32 * C::FN, c4 = 4 * (lane >> 5);
+  float s[C::FM];
 #pragma unroll
-  for (int i = 0; i < C::FM; ++i) {
-    const int row = m0 + wm * 32 * C::FM + 32 * i + (lane & 31), rc = min(row, p.T - 1);
-    const float s = row_gate(p.gate, rc);
+  for (int i = 0; i < C::FM; ++i) s[i] = row_gate(p.gate, min(r0 + 32 * i, p.T - 1));
+  struct Add { uint2 v[4]; };
+  each_fragment<C, Add, 8>(
+      [&](int i, int j, Add& ad) __attribute__((always_inline)) {   // rows and columns past the last read the last one
+        if (!p.add) return;
+        const uint16_t* row = (const uint16_t*)p.add + (size_t)min(r0 + 32 * i, p.T - 1) * p.H;
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j)
+        for (int v = 0; v < 4; ++v) ad.v[v] = *(const uint2*)(row + min(c00 + 32 * j + 8 * v, p.H - 8) + c4);
+      },
+      [&](int i, int j, const Add& ad) __attribute__((always_inline)) {
+        const int row = r0 + 32 * i;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int c = n0 + (wn * C::FN + j) * 32 + 16 * q;
-        float v[2][4];
+        for (int q = 0; q < 2; ++q) {
+          float v[2][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int ch = c + 8 * h + 4 * (lane >> 5);
-          uint2 ad = make_uint2(0, 0);
-          if (p.add && ch < p.H) ad = *(const uint2*)((const uint16_t*)p.add + (size_t)rc * p.H + ch);
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t w = e < 2 ? ad.x : ad.y;
-            v[h][e] = s * acc[i][j][8 * q + 4 * h + e] + __builtin_bit_cast(float, e & 1 ? w & 0xffff0000u : w << 16);
-          }
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t w = e < 2 ? ad.v[2 * q + h].x : ad.v[2 * q + h].y;
+              const float x = s[i] * acc[i][j][8 * q + 4 * h + e];
+              v[h][e] = p.add ? x + __builtin_bit_cast(float, e & 1 ? w & 0xffff0000u : w << 16) : x;
+            }
+          const u32x4 o = pack_pair(v[0], v[1]);
+          const int cc = c00 + 32 * j + 16 * q + 2 * c4;
+          if (row < p.T && cc < p.H) *(u32x4*)((uint16_t*)p.out + (size_t)row * p.H + cc) = o;
         }
-        const u32x4 o = pack_pair(v[0], v[1]);
-        const int cc = c + 8 * (lane >> 5);
-        if (row < p.T && cc < p.H) *(u32x4*)((uint16_t*)p.out + (size_t)row * p.H + cc) = o;
-      }
-  }
+      });
 }
 
 template <class C, bool A, bool Z>
 hipError_t run_gate_up(const FfnArgs& p, hipStream_t s) {
-  const auto k = ffn_gate_up_kernel<C, A, Z>;
+  const auto k = p.act && A ? ffn_gate_up_kernel<C, 1, A, Z> : ffn_gate_up_kernel<C, 0, A, Z>;
   return run_kernel("ffn_gate_up", s, [&] { k<<<tile_grid(p.mt, p.nt), C::NT, 0, s>>>(p); });
 }
 

@@ -155,36 +155,39 @@ __global__ __launch_bounds__(256, 1) void ortho_sym_kernel(SymArgs p) {
   uint16_t* out = p.out + (size_t)S * S * e;
   // panels [BM rows][64 columns] of LDS, 16-byte chunks permuted as in FragSrc
   const int r32 = lane & 31, x = (((r32 >> 1) & 1) << 2) | (((r32 >> 3) & 1) << 1);
+  struct Held { f16x4_t v[4]; };
+  const int c4 = 4 * (lane >> 5);
+  each_fragment<C, Held, 4>(
+      [&](int i, int j, Held& h) __attribute__((always_inline)) {   // rows and columns past the last read the last one
+        if (!QUAD) return;
+        const uint16_t* row = P + (size_t)min(m0 + wm * 32 * C::FM + 32 * i + r32, S - 1) * S;
 #pragma unroll
-  for (int i = 0; i < C::FM; ++i) {
-    const int tr = wm * 32 * C::FM + 32 * i + r32, row = m0 + tr, rc = min(row, S - 1);
+        for (int v = 0; v < 4; ++v) h.v[v] = *(const f16x4_t*)(row + min(n0 + (wn * C::FN + j) * 32 + 8 * v, S - 8) + c4);
+      },
+      [&](int i, int j, const Held& held) __attribute__((always_inline)) {
+        const int tr = wm * 32 * C::FM + 32 * i + r32, row = m0 + tr;
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j)
+        for (int q = 0; q < 2; ++q) {
+          const int tc = (wn * C::FN + j) * 32 + 16 * q;
+          float v[2][4];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int tc = (wn * C::FN + j) * 32 + 16 * q;
-        float v[2][4];
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          f16x4_t pv = {0, 0, 0, 0};
-          const int c = n0 + tc + 8 * h + 4 * (lane >> 5);
-          if (QUAD && c < S) pv = *(const f16x4_t*)(P + (size_t)rc * S + c);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float s = acc[i][j][8 * q + 4 * h + k];
-            v[h][k] = QUAD ? p.b * (float)pv[k] + p.c * s : s;
+            for (int k = 0; k < 4; ++k) {
+              const float s = acc[i][j][8 * q + 4 * h + k];
+              v[h][k] = QUAD ? p.b * (float)held.v[2 * q + h][k] + p.c * s : s;
+            }
+            if (mt != nt) {
+              const int ct = tc + 8 * h;
+              *(uint2*)(lds + (ct >> 6) * (C::BM * 128) + tr * 128 + ((((ct >> 3) & 7) ^ x) << 4) + 2 * c4) =
+                  make_uint2(pack_f16(v[h][0], v[h][1]), pack_f16(v[h][2], v[h][3]));
+            }
           }
-          if (mt != nt) {
-            const int ct = tc + 8 * h;
-            *(uint2*)(lds + (ct >> 6) * (C::BM * 128) + tr * 128 + ((((ct >> 3) & 7) ^ x) << 4) + 8 * (lane >> 5)) =
-                make_uint2(pack_f16(v[h][0], v[h][1]), pack_f16(v[h][2], v[h][3]));
-          }
+          const u32x4 o = pack_pair_f16(v[0], v[1]);
+          const int cc = n0 + tc + 2 * c4;
+          if (row < S && cc < S) *(u32x4*)(out + (size_t)row * S + cc) = o;
         }
-        const u32x4 o = pack_pair_f16(v[0], v[1]);
-        const int cc = n0 + tc + 8 * (lane >> 5);
-        if (row < S && cc < S) *(u32x4*)(out + (size_t)row * S + cc) = o;
-      }
-  }
+      });
   if (mt == nt) return;
   __syncthreads();
   // 32 columns x 16 rows a read: lane -> column lane % 32, rows 8 (lane / 32) .. + 7
@@ -256,47 +259,51 @@ __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
   // the products carry ORTHO_X ORTHO_P, x ORTHO_X
   const float fx = TO == TO_X ? p.a : p.a / ORTHO_X, fs = TO == TO_X ? 1.f / ORTHO_P : 1.f / (ORTHO_X * ORTHO_P);
   const size_t at = (size_t)M * N * e;
+  const int r0 = m0 + wm * 32 * C::FM + (lane & 31), c00 = n0 + wn * 32 * C::FN, c4 = 4 * (lane >> 5);
+  const bool step = TO != TO_X && p.w != nullptr;
+  struct Held { f16x4_t x[4]; float w[TO == TO_X ? 1 : 4][4]; };
+  each_fragment<C, Held, (TO == TO_X ? 4 : 2)>(
+      [&](int i, int j, Held& h) __attribute__((always_inline)) {   // rows and columns past the last read the last one
+        const size_t row = (size_t)min(r0 + 32 * i, M - 1) * N;
 #pragma unroll
-  for (int i = 0; i < C::FM; ++i) {
-    const int row = m0 + wm * 32 * C::FM + 32 * i + (lane & 31), rc = min(row, M - 1);
-#pragma unroll
-    for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int c = n0 + (wn * C::FN + j) * 32 + 16 * q;
-        float v[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int ch = min(c + 8 * h, N - 8) + 4 * (lane >> 5);
-          const f16x4_t xv = *(const f16x4_t*)(X + (size_t)rc * N + ch);
-          float w[4] = {0.f, 0.f, 0.f, 0.f};
-          if (TO != TO_X && p.w) load4((const T*)p.w + at + (size_t)rc * N + ch, w);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float o = fx * (float)xv[k] + fs * acc[i][j][8 * q + 4 * h + k];
-            v[h][k] = TO != TO_X && p.w ? p.keep * w[k] - p.lr * o : o;
-          }
+        for (int v = 0; v < 4; ++v) {
+          const size_t el = row + min(c00 + 32 * j + 8 * v, N - 8) + c4;
+          h.x[v] = *(const f16x4_t*)(X + el);
+          if (TO != TO_X && step) load4((const T*)p.w + at + el, h.w[v]);
         }
-        if constexpr (TO == TO_F32) {
+      },
+      [&](int i, int j, const Held& held) __attribute__((always_inline)) {
+        const int row = r0 + 32 * i;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int ch = c + 8 * h + 4 * (lane >> 5);
-            if (row < M && ch < N) store4<float>((float*)p.out + at + (size_t)row * N + ch, v[h][0], v[h][1], v[h][2], v[h][3]);
-          }
-        } else {
-          u32x4 o;
-          if constexpr (TO == TO_X) {
-            o = pack_pair_f16(v[0], v[1]);
+        for (int q = 0; q < 2; ++q) {
+          const int c = c00 + 32 * j + 16 * q;
+          float v[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float o = fx * (float)held.x[2 * q + h][k] + fs * acc[i][j][8 * q + 4 * h + k];
+              v[h][k] = step ? p.keep * held.w[TO == TO_X ? 0 : 2 * q + h][k] - p.lr * o : o;
+            }
+          if constexpr (TO == TO_F32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (row < M && c + 8 * h < N)
+                store4<float>((float*)p.out + at + (size_t)row * N + c + 8 * h + c4, v[h][0], v[h][1], v[h][2], v[h][3]);
           } else {
-            const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16(v[0][0], v[0][1]), pack_bf16(v[1][0], v[1][1]), false, false);
-            const auto b = __builtin_amdgcn_permlane32_swap(pack_bf16(v[0][2], v[0][3]), pack_bf16(v[1][2], v[1][3]), false, false);
-            o = u32x4{a[0], b[0], a[1], b[1]};
+            u32x4 o;
+            if constexpr (TO == TO_X) {
+              o = pack_pair_f16(v[0], v[1]);
+            } else {
+              const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16(v[0][0], v[0][1]), pack_bf16(v[1][0], v[1][1]), false, false);
+              const auto b = __builtin_amdgcn_permlane32_swap(pack_bf16(v[0][2], v[0][3]), pack_bf16(v[1][2], v[1][3]), false, false);
+              o = u32x4{a[0], b[0], a[1], b[1]};
+            }
+            const int cc = c + 2 * c4;
+            if (row < M && cc < N) *(u32x4*)((uint16_t*)p.out + at + (size_t)row * N + cc) = o;
           }
-          const int cc = c + 8 * (lane >> 5);
-          if (row < M && cc < N) *(u32x4*)((uint16_t*)p.out + at + (size_t)row * N + cc) = o;
         }
-      }
-  }
+      });
 }
 
 // ------------------------------------------------------------------ host
