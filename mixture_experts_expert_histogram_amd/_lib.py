@@ -630,14 +630,6 @@ def _kind(t, name: str) -> int:
     return MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32
 
 
-def _device_rows(t, name: str):
-    """(T, H) of a contiguous device tensor [T, H]."""
-    if not t.is_cuda or t.dim() != 2:
-        raise ValueError(f"{name} must be a device tensor [T, H]")
-    _need(t, name, t.shape, t.dtype, t.device)
-    return tuple(t.shape)
-
-
 def _workspace(ws, nbytes: int, device):
     import torch
     if ws is None:
@@ -645,12 +637,6 @@ def _workspace(ws, nbytes: int, device):
     if ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws must be contiguous, on {device}")
     return ws
-
-
-def _optional(t, name: str, shape, dtype, device):
-    if t is not None:
-        _need(t, name, shape, dtype, device)
-    return _ptr(t)
 
 
 def _result(t, name: str, shape, dtype, device):
@@ -662,18 +648,29 @@ def _result(t, name: str, shape, dtype, device):
     return t
 
 
-_block_sizes = {}
+_native = None
 
 
-def _sized(make, size_of, *key):
-    """(descriptor, sizes) of a call, kept by the descriptor's values (at most 4096 of them)."""
-    got = _block_sizes.get((size_of, key))
-    if got is None:
-        d = make(*key)
-        if len(_block_sizes) >= 4096:
-            _block_sizes.clear()
-        got = _block_sizes[(size_of, key)] = (d, size_of(d))
-    return got
+def _block():
+    """The native half of the binding of these operators (csrc/binding.cpp): checks, outputs and the call."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (its libraries, which the module is linked to)
+        library()
+        from . import _block as native
+        native.init(_check, _raw_stream)
+        _native = native
+    return _native
+
+
+_ACTS, _LAYOUTS = {"swiglu": MOE_SWIGLU, "clamped": MOE_CLAMPED_GLU}, {"concat": MOE_GU_CONCAT, "interleaved": MOE_GU_INTERLEAVED}
+
+
+def _codes(act, layout):
+    try:
+        return _ACTS[act], _LAYOUTS[layout]
+    except KeyError:
+        raise ValueError(f"unknown act {act!r} or layout {layout!r}") from None
 
 
 def ffn_workspace_size(desc: MoeDesc) -> Tuple[int, int, int]:
@@ -684,58 +681,21 @@ def ffn_workspace_size(desc: MoeDesc) -> Tuple[int, int, int]:
     return f.value, b.value, s.value
 
 
-def _ffn(x, w_gate_up, w_down, gate, act, layout, limit, alpha, grad_dtype):
-    import torch
-    T, H = _device_rows(x, "x")
-    if act not in ("swiglu", "clamped") or layout not in ("concat", "interleaved"):
-        raise ValueError(f"unknown act {act!r} or layout {layout!r}")
-    if w_gate_up.dim() != 2 or w_gate_up.shape[0] % 2:
-        raise ValueError("w_gate_up must be [2I, H]")
-    I = w_gate_up.shape[0] // 2
-    _need(w_gate_up, "w_gate_up", (2 * I, H), x.dtype, x.device)
-    _need(w_down, "w_down", (H, I), x.dtype, x.device)
-    _optional(gate, "gate", (T,), torch.float32, x.device)
-    dt = "bf16" if _kind(x, "x") == MOE_BF16 else "fp32"
-    return (I,) + _sized(make_desc, ffn_workspace_size, T, H, I, 1, 1, dt, act, layout, float(limit), float(alpha),
-                         grad_dtype or dt)
-
-
 def ffn_fwd(x, w_gate_up, w_down, gate=None, add=None, act="swiglu", layout="concat", limit=7.0, alpha=1.702, save=False,
             ws=None, out=None, saved=None):
     """Gated feed-forward block of every token (a shared expert, a dense layer):
     add + sigmoid(gate) Wd phi(Wgu x) for x [T,H], w_gate_up [2I,H], w_down [H,I], gate fp32 [T], add [T,H].
     Returns (out, saved-or-None, ws); `out` may be `add`."""
-    I, d, (nbytes, _, sbytes) = _ffn(x, w_gate_up, w_down, gate, act, layout, limit, alpha, None)
-    dev = x.device
-    add_p = _optional(add, "add", x.shape, x.dtype, dev)
-    ws = _workspace(ws, nbytes, dev)
-    out = _result(out, "out", x.shape, x.dtype, dev)
-    if save and saved is None:
-        saved = empty_workspace(sbytes, dev)
-    _launch(dev, "moe_ffn_fwd", library().moe_ffn_fwd, ctypes.byref(d), _ptr(x), _ptr(w_gate_up), _ptr(w_down), _ptr(gate),
-            add_p, _ptr(out), _ptr(saved) if save else None, _nbytes(saved) if save else 0, _ptr(ws), _nbytes(ws))
-    return out, (saved if save else None), ws
+    return (_native or _block()).ffn_fwd(x, w_gate_up, w_down, gate, *_codes(act, layout), limit, alpha, add, save, ws, out,
+                                         saved)
 
 
 def ffn_bwd(x, w_gate_up, w_down, d_out, saved=None, gate=None, act="swiglu", layout="concat", limit=7.0, alpha=1.702,
             ws=None, grads=None, grad_dtype=None):
     """Backward pass of ffn_fwd; returns (d_x, d_gate-or-None, d_w_gate_up, d_w_down, ws).  The gradient of `add` is
     d_out.  grad_dtype: "bf16" or "fp32" storage of the weight gradients (default: the activation dtype)."""
-    import torch
-    I, d, (_, nbytes, _) = _ffn(x, w_gate_up, w_down, gate, act, layout, limit, alpha, grad_dtype)
-    dev = x.device
-    T, H = x.shape
-    _need(d_out, "d_out", x.shape, x.dtype, dev)
-    ws = _workspace(ws, nbytes, dev)
-    gdt = torch.float32 if d.grad_dtype == MOE_F32 else torch.bfloat16
-    dx, dg, dgu, dd = grads if grads is not None else (None,) * 4
-    dx = _result(dx, "d_x", x.shape, x.dtype, dev)
-    dg = _result(dg, "d_gate", (T,), torch.float32, dev) if gate is not None else None
-    dgu = _result(dgu, "d_w_gate_up", (2 * I, H), gdt, dev)
-    dd = _result(dd, "d_w_down", (H, I), gdt, dev)
-    _launch(dev, "moe_ffn_bwd", library().moe_ffn_bwd, ctypes.byref(d), _ptr(x), _ptr(w_gate_up), _ptr(w_down), _ptr(gate),
-            _ptr(d_out), _ptr(saved), _nbytes(saved), _ptr(dx), _ptr(dg), _ptr(dgu), _ptr(dd), _ptr(ws), _nbytes(ws))
-    return dx, dg, dgu, dd, ws
+    return (_native or _block()).ffn_bwd(x, w_gate_up, w_down, gate, *_codes(act, layout), limit, alpha, d_out, saved,
+                                         -1 if grad_dtype is None else _dt(grad_dtype), ws, *(grads or (None,) * 4))
 
 
 GATE_NONE, GATE_ROW, GATE_COLUMN, GATE_FULL = range(4)   # moe_gate_t
@@ -745,63 +705,22 @@ def norm_workspace_size(desc: NormDesc) -> int:
     return _size_of(library().moe_norm_workspace_size, desc, "moe_norm_workspace_size")
 
 
-def _norm(x, kind, scale, eps):
-    T, H = _device_rows(x, "x")
-    return _sized(NormDesc, norm_workspace_size, T, H, _kind(x, "x"), kind, float(scale), float(eps))
-
-
 def norm_fwd(x, w, eps=1e-5, out=None):
     """w x / rms(x) of each row of x [T,H]; w [H] of x's type."""
-    d, _ = _norm(x, GATE_NONE, 1.0, eps)
-    _need(w, "w", x.shape[1:], x.dtype, x.device)
-    out = _result(out, "out", x.shape, x.dtype, x.device)
-    _launch(x.device, "moe_norm_fwd", library().moe_norm_fwd, ctypes.byref(d), _ptr(x), _ptr(w), _ptr(out))
-    return out
+    return (_native or _block()).norm_fwd(x, w, eps, out)
 
 
 def norm_bwd(x, w, d_y, d_add=None, eps=1e-5, ws=None, grads=None):
     """Backward pass of norm_fwd; d_add [T,H], the gradient that reaches x beside the norm, is added to d_x.
     Returns (d_x, d_w fp32 [H], ws); d_x may be d_add."""
-    import torch
-    d, nbytes = _norm(x, GATE_NONE, 1.0, eps)
-    dev = x.device
-    _need(w, "w", x.shape[1:], x.dtype, dev)
-    _need(d_y, "d_y", x.shape, x.dtype, dev)
-    add_p = _optional(d_add, "d_add", x.shape, x.dtype, dev)
-    ws = _workspace(ws, nbytes, dev)
-    dx, dw = grads if grads is not None else (None, None)
-    dx = _result(dx, "d_x", x.shape, x.dtype, dev)
-    dw = _result(dw, "d_w", x.shape[1:], torch.float32, dev)
-    _launch(dev, "moe_norm_bwd", library().moe_norm_bwd, ctypes.byref(d), _ptr(x), _ptr(w), _ptr(d_y), add_p, _ptr(dx),
-            _ptr(dw), _ptr(ws), _nbytes(ws))
-    return dx, dw, ws
-
-
-def _gate_kind(gate, x) -> int:
-    T, H = x.shape
-    if gate is None:
-        return GATE_NONE
-    for kind, shape in ((GATE_ROW, (T, 1)), (GATE_COLUMN, (H,)), (GATE_FULL, (T, H))):
-        if tuple(gate.shape) == shape:
-            _need(gate, "gate", shape, x.dtype, x.device)
-            return kind
-    raise ValueError(f"gate must be [T, 1], [H] or [T, H], got {tuple(gate.shape)}")
+    return (_native or _block()).norm_bwd(x, w, d_y, d_add, eps, ws, *(grads or (None, None)))
 
 
 def residual_fwd(x, h, w_post=None, gate=None, scale=1.0, w_next=None, eps=1e-5, x_new=None, y=None):
     """The step after a block: x_new = x + scale gate n with n = w_post h / rms(h) (h without w_post), and the next
     block's norm y = w_next x_new / rms(x_new) (None without w_next).  x, h [T,H]; w_post, w_next [H]; gate [T,1], [H]
     or [T,H]; all of one type.  Returns (x_new, y); x_new may be x."""
-    kind = _gate_kind(gate, x) if x.dim() == 2 else GATE_NONE
-    d, _ = _norm(x, kind, scale, eps)
-    dev, H = x.device, x.shape[1:]
-    _need(h, "h", x.shape, x.dtype, dev)
-    post_p, next_p = _optional(w_post, "w_post", H, x.dtype, dev), _optional(w_next, "w_next", H, x.dtype, dev)
-    x_new = _result(x_new, "x_new", x.shape, x.dtype, dev)
-    y = _result(y, "y", x.shape, x.dtype, dev) if w_next is not None else None
-    _launch(dev, "moe_residual_fwd", library().moe_residual_fwd, ctypes.byref(d), _ptr(x), _ptr(h), post_p, _ptr(gate),
-            next_p, _ptr(x_new), _ptr(y))
-    return x_new, y
+    return (_native or _block()).residual_fwd(x, h, w_post, gate, scale, w_next, eps, x_new, y)
 
 
 class ResidualGrads(NamedTuple):
@@ -819,25 +738,8 @@ def residual_bwd(x_new, h, d_x_new=None, d_y=None, w_post=None, gate=None, scale
                  grads: Optional[ResidualGrads] = None) -> ResidualGrads:
     """Backward pass of residual_fwd, given its x_new and the gradients of x_new (None: zero) and, with w_next, of y.
     grads: where to put the results (its ws is not used)."""
-    import torch
-    kind = _gate_kind(gate, x_new) if x_new.dim() == 2 else GATE_NONE
-    d, nbytes = _norm(x_new, kind, scale, eps)
-    dev, dt, rows, H = x_new.device, x_new.dtype, x_new.shape, x_new.shape[1:]
-    _need(h, "h", rows, dt, dev)
-    if (w_next is None) != (d_y is None):
-        raise ValueError("d_y goes with w_next")
-    post_p, next_p = _optional(w_post, "w_post", H, dt, dev), _optional(w_next, "w_next", H, dt, dev)
-    new_p, dy_p = _optional(d_x_new, "d_x_new", rows, dt, dev), _optional(d_y, "d_y", rows, dt, dev)
-    ws = _workspace(ws, nbytes, dev)
-    given = grads if grads is not None else ResidualGrads(*(None,) * 6)
-    dx = _result(given.d_x, "d_x", rows, dt, dev)
-    dh = _result(given.d_h, "d_h", rows, dt, dev)
-    dg = None if gate is None else _result(given.d_gate, "d_gate", gate.shape, dt if kind == GATE_FULL else torch.float32, dev)
-    dpost = None if w_post is None else _result(given.d_w_post, "d_w_post", H, torch.float32, dev)
-    dnext = None if w_next is None else _result(given.d_w_next, "d_w_next", H, torch.float32, dev)
-    _launch(dev, "moe_residual_bwd", library().moe_residual_bwd, ctypes.byref(d), _ptr(x_new), _ptr(h), post_p, _ptr(gate),
-            next_p, new_p, dy_p, _ptr(dx), _ptr(dh), _ptr(dg), _ptr(dpost), _ptr(dnext), _ptr(ws), _nbytes(ws))
-    return ResidualGrads(dx, dh, dg, dpost, dnext, ws)
+    return ResidualGrads._make((_native or _block()).residual_bwd(x_new, h, d_x_new, d_y, w_post, gate, scale, w_next, eps, ws,
+                                                                  *(grads[:5] if grads else (None,) * 5)))
 
 
 NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)   # the usual coefficients
@@ -856,7 +758,8 @@ def _ortho(g, name, out_dtype, steps, coef, eps):
     for n in g.shape[:-2]:
         E *= n
     a, b, c = (float(v) for v in coef)
-    return _sized(OrthoDesc, ortho_workspace_size, E, M, N, _kind(g, name), out_dtype, int(steps), a, b, c, float(eps))
+    d = OrthoDesc(E, M, N, _kind(g, name), out_dtype, int(steps), a, b, c, float(eps))
+    return d, ortho_workspace_size(d)
 
 
 def orthogonalize(g, steps=5, coef=NEWTON_SCHULZ, eps=1e-7, dtype="bf16", ws=None, out=None):

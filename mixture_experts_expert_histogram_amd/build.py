@@ -14,6 +14,7 @@ LIB_NAME = "libmoe_mi355x.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["route.hip", "gemm.hip", "gemm_dma.hip", "gemm_mx.hip", "few.hip", "mx.hip", "ffn_fwd.hip",
            "ffn_bwd.hip", "ffn_few.hip", "norm.hip", "ortho.hip", "api.cpp", "api_block.cpp"]
+BINDING, BINDING_NAME = "binding.cpp", "_block.so"   # the native half of the Python binding
 ARCH = "gfx950"
 
 
@@ -30,6 +31,20 @@ def compile_flags():
             "-I", os.path.join(ROOT, "include"), "-Wno-unused-result", "-Wno-inline-asm"]
 
 
+def binding_commands(obj: str, out: str):
+    """g++ on the CPython module of the operators around the routed experts (torch's headers and libraries): compile, link."""
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__", "-c", os.path.join(CSRC, BINDING), "-o", obj,
+             "-I", os.path.join(t, "include"), "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+             "-I", sysconfig.get_paths()["include"], "-I", os.path.join(rocm, "include")],
+            ["g++", "-shared", obj, "-o", out, "-L", os.path.join(t, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python",
+             "-Wl,-rpath," + os.path.join(t, "lib"), LIB_PATH, "-Wl,-rpath,$ORIGIN"])
+
+
 def build(verbose: bool = False) -> str:
     """Always recompiles every source and relinks the shared library."""
     os.makedirs(BUILD, exist_ok=True)
@@ -43,6 +58,9 @@ def build(verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    binding = os.path.join(PKG, BINDING_NAME)
+    compile_binding, link_binding = binding_commands(os.path.join(BUILD, BINDING + ".o"), binding + ".tmp")
+    procs.append((BINDING, subprocess.Popen(compile_binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out = p.communicate()[0].decode(errors="replace")
@@ -55,9 +73,11 @@ def build(verbose: bool = False) -> str:
     if failed:
         raise RuntimeError("HIP compilation failed: " + ", ".join(failed))
     tmp = LIB_PATH + ".tmp"
-    cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
+    cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname," + LIB_NAME, "-o", tmp] + objs
     subprocess.check_call(cmd)
     os.replace(tmp, LIB_PATH)
+    subprocess.check_call(link_binding)
+    os.replace(binding + ".tmp", binding)
     return LIB_PATH
 
 
