@@ -132,12 +132,12 @@ __global__ __launch_bounds__(FEW_NW * 64) void ffn_few_down_kernel(FfnArgs p) {
   }
 }
 
-// ------------------------------------------------------------------ one token
+// ------------------------------------------------------------------ up to four tokens
 // A wave takes one activation column (its gate and its up row) or one output
 // row, a lane 16 bytes of every kilobyte of a row: nothing is shared between
 // waves, and at 2880 columns every load of the card is in flight at once, 11
-// waves a CU.  2880 x 2880 bf16: 16-row workgroups took 12.5 and 6.6 us for the
-// two kernels (104 of 256 CUs had two workgroups, the others one).
+// waves a CU.  2880 x 2880 bf16, one token: 7.3 and 4.6 us (4.6 and 3.6 TB/s)
+// for the two kernels, where the 16-row workgroups took 12.5 and 6.6.
 constexpr int ONE_CH = 6;   // kilobytes of a row in flight
 
 template <bool F32>
@@ -154,15 +154,17 @@ __device__ __forceinline__ float dot16(u32x4 w, u32x4 x, float s) {
   }
   return s;
 }
-// This lane's part of the dot products of R rows (of `bytes` bytes, from w[r])
-// with x, summed over the wave.
-template <bool F32, int R>
-__device__ __forceinline__ void one_dot(const __amdgpu_buffer_rsrc_t (&w)[R], __amdgpu_buffer_rsrc_t x, uint32_t bytes, int lane,
-                                        float (&sum)[R]) {
+// The dot products of R rows (of `bytes` bytes, from w[r]) with the first N of
+// T tokens (rows of x), in every lane.
+template <bool F32, int R, int N>
+__device__ __forceinline__ void one_dot(const __amdgpu_buffer_rsrc_t (&w)[R], __amdgpu_buffer_rsrc_t x, int T, uint32_t bytes,
+                                        int lane, float (&sum)[R][N]) {
 #pragma unroll
-  for (int r = 0; r < R; ++r) sum[r] = 0.f;
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < N; ++t) sum[r][t] = 0.f;
   for (uint32_t c0 = 0; c0 < bytes; c0 += ONE_CH * 1024) {
-    u32x4 wv[R][ONE_CH], xv[ONE_CH];
+    u32x4 wv[R][ONE_CH], xv[N][ONE_CH];
 #pragma unroll
     for (int c = 0; c < ONE_CH; ++c) {
       const uint32_t o = c0 + c * 1024 + lane * 16, at = o < bytes ? o : kNone;
@@ -172,45 +174,60 @@ __device__ __forceinline__ void one_dot(const __amdgpu_buffer_rsrc_t (&w)[R], __
 #pragma unroll
     for (int c = 0; c < ONE_CH; ++c) {
       const uint32_t o = c0 + c * 1024 + lane * 16;
-      xv[c] = load16(x, o < bytes ? o : kNone);
+#pragma unroll
+      for (int t = 0; t < N; ++t) xv[t][c] = load16(x, o < bytes && t < T ? t * bytes + o : kNone);
     }
 #pragma unroll
     for (int c = 0; c < ONE_CH; ++c)
 #pragma unroll
-      for (int r = 0; r < R; ++r) sum[r] = dot16<F32>(wv[r][c], xv[c], sum[r]);
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < N; ++t) sum[r][t] = dot16<F32>(wv[r][c], xv[t][c], sum[r][t]);
   }
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1)
 #pragma unroll
-    for (int r = 0; r < R; ++r) sum[r] += __shfl_xor(sum[r], d);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < N; ++t) sum[r][t] += __shfl_xor(sum[r][t], d);
 }
 
-template <bool F32>
+template <bool F32, int N>
 __global__ __launch_bounds__(256) void ffn_one_gate_up_kernel(FfnArgs p) {
   using T = std::conditional_t<F32, float, uint16_t>;
   const int lane = threadIdx.x & 63, j = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // I is a multiple of 8
   const __amdgpu_buffer_rsrc_t w[2] = {rsrc((const T*)p.gu_g + p.gu_rs * j), rsrc((const T*)p.gu_u + p.gu_rs * j)};
-  float s[2];
-  one_dot<F32, 2>(w, rsrc(p.x), p.H * sizeof(T), lane, s);
-  if (lane == 0) store_val<T>((T*)p.a + j, glu_fwd(s[0], s[1], p.act, p.limit, p.alpha));
+  float s[2][N];
+  one_dot<F32, 2, N>(w, rsrc(p.x), p.T, p.H * sizeof(T), lane, s);
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+    if (lane == 0 && t < p.T) store_val<T>((T*)p.a + (size_t)t * p.I + j, glu_fwd(s[0][t], s[1][t], p.act, p.limit, p.alpha));
 }
 
-template <bool F32>
+template <bool F32, int N>
 __global__ __launch_bounds__(256) void ffn_one_down_kernel(FfnArgs p) {
   using T = std::conditional_t<F32, float, uint16_t>;
   const int lane = threadIdx.x & 63, h = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // so is H
   const __amdgpu_buffer_rsrc_t w[1] = {rsrc((const T*)p.wd + (size_t)p.I * h)};
-  const float ad = p.add ? as_float(((const T*)p.add)[h]) : 0.f, g = row_gate(p.gate, 0);
-  float s[1];
-  one_dot<F32, 1>(w, rsrc(p.a), p.I * sizeof(T), lane, s);
-  if (lane == 0) store_val<T>((T*)p.out + h, ad + g * s[0]);
+  float ad[N], g[N];
+#pragma unroll
+  for (int t = 0; t < N; ++t) {
+    const int tc = min(t, p.T - 1);
+    ad[t] = p.add ? as_float(((const T*)p.add)[(size_t)tc * p.H + h]) : 0.f;
+    g[t] = row_gate(p.gate, tc);
+  }
+  float s[1][N];
+  one_dot<F32, 1, N>(w, rsrc(p.a), p.T, p.I * sizeof(T), lane, s);
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+    if (lane == 0 && t < p.T) store_val<T>((T*)p.out + (size_t)t * p.H + h, ad[t] + g[t] * s[0][t]);
 }
 
-template <bool F32>
+template <bool F32, int N>
 hipError_t run_one(const FfnArgs& p, hipStream_t s) {
-  const hipError_t e = run_kernel("ffn_one_gate_up", s, [&] { ffn_one_gate_up_kernel<F32><<<p.I / 4, 256, 0, s>>>(p); });
+  const hipError_t e = run_kernel("ffn_one_gate_up", s, [&] { ffn_one_gate_up_kernel<F32, N><<<p.I / 4, 256, 0, s>>>(p); });
   if (e != hipSuccess) return e;
-  return run_kernel("ffn_one_down", s, [&] { ffn_one_down_kernel<F32><<<p.H / 4, 256, 0, s>>>(p); });
+  return run_kernel("ffn_one_down", s, [&] { ffn_one_down_kernel<F32, N><<<p.H / 4, 256, 0, s>>>(p); });
 }
 
 template <bool F32, int NT>
@@ -218,6 +235,14 @@ hipError_t run_few(const FfnArgs& p, hipStream_t s) {
   const hipError_t e = run_kernel("ffn_few_gate_up", s, [&] { ffn_few_gate_up_kernel<F32, NT><<<p.I / 8, FEW_NW * 64, 0, s>>>(p); });
   if (e != hipSuccess) return e;
   return run_kernel("ffn_few_down", s, [&] { ffn_few_down_kernel<F32, NT><<<(p.H + 15) / 16, FEW_NW * 64, 0, s>>>(p); });
+}
+
+template <bool F32>
+hipError_t few(const FfnArgs& p, hipStream_t s) {
+  if (p.T == 1) return run_one<F32, 1>(p, s);
+  if (p.T == 2) return run_one<F32, 2>(p, s);
+  if (p.T <= 4) return run_one<F32, 4>(p, s);
+  return p.T <= 16 ? run_few<F32, 1>(p, s) : p.T <= 32 ? run_few<F32, 2>(p, s) : run_few<F32, 4>(p, s);
 }
 
 // ------------------------------------------------------------------ the block as one expert (fp32, many tokens)
@@ -240,11 +265,7 @@ __global__ __launch_bounds__(256) void ffn_dgate_kernel(const float* w, const fl
 
 using namespace dense;
 
-hipError_t launch_ffn_few(int dtype, FfnArgs p, hipStream_t s) {
-  if (p.T == 1) return dtype == 0 ? run_one<false>(p, s) : run_one<true>(p, s);
-  if (dtype == 0) return p.T <= 16 ? run_few<false, 1>(p, s) : p.T <= 32 ? run_few<false, 2>(p, s) : run_few<false, 4>(p, s);
-  return p.T <= 16 ? run_few<true, 1>(p, s) : p.T <= 32 ? run_few<true, 2>(p, s) : run_few<true, 4>(p, s);
-}
+hipError_t launch_ffn_few(int dtype, FfnArgs p, hipStream_t s) { return dtype == 0 ? few<false>(p, s) : few<true>(p, s); }
 
 hipError_t launch_ffn_one_expert(const float* gate, int T, int32_t* ids, float* w, hipStream_t s) {
   return run_kernel("ffn_one_expert", s, [&] { ffn_one_expert_kernel<<<(T + 255) / 256, 256, 0, s>>>(gate, T, ids, w); });

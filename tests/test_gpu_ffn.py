@@ -71,13 +71,13 @@ def run(d, act="swiglu", layout="concat", grad_dtype=None, backward=True):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 32, 33, 64, 65, 127, 129, 300])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 15, 16, 17, 32, 33, 64, 65, 127, 129, 300])
 def test_token_counts(T, dtype):
     run(inputs(T, 136, 72, dtype, seed=T), "clamped", "interleaved")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("T", [5, 70])
+@pytest.mark.parametrize("T", [1, 3, 5, 70])
 @pytest.mark.parametrize("H,I", [(8, 8), (8, 264), (264, 8), (16, 24), (64, 64), (72, 136), (192, 320), (1048, 712), (200, 1032)])
 def test_sizes(T, H, I, dtype):
     run(inputs(T, H, I, dtype, seed=H + I, gated=I % 16 == 8))
