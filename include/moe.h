@@ -337,8 +337,9 @@ moe_status_t moe_mx_fwd_logits(const moe_desc_t* desc, const void* hidden,
  *   - H and I at most 2^20 and H I at most 2^28, else MOE_ERR_UNSUPPORTED.
  *   - a = phi(..) is rounded to the activations' type as the second product's
  *     operand; sums are fp32; out is rounded once.
- *   - Up to 64 tokens without `saved` run on kernels that read the weights
- *     once and make no tiles; their order of sums is their own.
+ *   - Up to 16 tokens (bf16) or 64 (fp32) without `saved` run on kernels that
+ *     read the weights once and make no tiles; their order of sums is their
+ *     own.
  *   - `saved` (nullable) receives the gate and up values (fp32, in an order of
  *     the library's) for moe_ffn_bwd; saved_bytes below the required size:
  *     MOE_ERR_WORKSPACE.

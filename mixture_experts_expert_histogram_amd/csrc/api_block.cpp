@@ -201,7 +201,8 @@ moe_status_t moe_ffn_fwd(const moe_desc_t* desc, const void* x, const void* w_ga
   p.a = b + L.a;
   p.add = add;
   p.out = out;
-  if (desc->T <= FFN_FEW_T && !saved) return launched(launch_ffn_few(desc->dtype == MOE_BF16 ? 0 : 1, p, stream));
+  if (desc->T <= (L.one_expert ? FFN_FEW_F32 : FFN_FEW_BF16) && !saved)
+    return launched(launch_ffn_few(L.one_expert ? 1 : 0, p, stream));
   if (!L.one_expert) {
     p.z = (float*)saved;
     TRY(launched(launch_ffn_gate_up(p, stream)));

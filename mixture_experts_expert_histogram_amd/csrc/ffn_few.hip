@@ -1,4 +1,4 @@
-// The gated feed-forward block for up to 64 tokens, bf16 or fp32: the time is
+// The gated feed-forward block for up to 16 tokens (bf16) or 64 (fp32): the time is
 // that of reading 3 H I weights once, and for one token that of two launches and
 // their first loads.
 //
@@ -242,7 +242,11 @@ hipError_t few(const FfnArgs& p, hipStream_t s) {
   if (p.T == 1) return run_one<F32, 1>(p, s);
   if (p.T == 2) return run_one<F32, 2>(p, s);
   if (p.T <= 4) return run_one<F32, 4>(p, s);
-  return p.T <= 16 ? run_few<F32, 1>(p, s) : p.T <= 32 ? run_few<F32, 2>(p, s) : run_few<F32, 4>(p, s);
+  if constexpr (F32) {
+    if (p.T > 32) return run_few<F32, 4>(p, s);
+    if (p.T > 16) return run_few<F32, 2>(p, s);
+  }
+  return run_few<F32, 1>(p, s);
 }
 
 // ------------------------------------------------------------------ the block as one expert (fp32, many tokens)
