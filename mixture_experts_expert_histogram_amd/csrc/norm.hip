@@ -27,7 +27,11 @@ namespace {
 enum { GATE_NONE = 0, GATE_ROW = 1, GATE_COLUMN = 2, GATE_FULL = 3 };
 constexpr int V = 2;   // groups of 8 elements a thread
 
-// 8 consecutive elements as they lie in memory.
+// 8 consecutive elements as they lie in memory.  Stores are non-temporal: rows
+// are written once and L2 keeps what is read (the backward pass of 32768 rows of
+// 4096 308 -> 291 us, of 4096 rows of 2880 20.9 -> 19.6).
+typedef uint32_t u32x4_nt __attribute__((ext_vector_type(4)));
+typedef float f32x4_nt __attribute__((ext_vector_type(4)));
 template <typename T> struct Raw;
 template <> struct Raw<uint16_t> {
   uint4 v;
@@ -42,7 +46,8 @@ template <> struct Raw<uint16_t> {
     }
   }
   static __device__ __forceinline__ void store(uint16_t* p, const float* f) {
-    *(uint4*)p = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    const u32x4_nt v = {pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+    __builtin_nontemporal_store(v, (u32x4_nt*)p);
   }
 };
 template <> struct Raw<float> {
@@ -54,8 +59,8 @@ template <> struct Raw<float> {
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   }
   static __device__ __forceinline__ void store(float* p, const float* f) {
-    *(float4*)p = make_float4(f[0], f[1], f[2], f[3]);
-    *(float4*)(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    __builtin_nontemporal_store(f32x4_nt{f[0], f[1], f[2], f[3]}, (f32x4_nt*)p);
+    __builtin_nontemporal_store(f32x4_nt{f[4], f[5], f[6], f[7]}, (f32x4_nt*)(p + 4));
   }
 };
 __device__ __forceinline__ float one_value(const uint16_t* p) { return __builtin_bit_cast(float, (uint32_t)*p << 16); }
@@ -281,9 +286,13 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs p) {
   for (int j = 0; j < V; ++j) {
     const int col = column(j);
     if (col >= H) continue;
-    if (next) Raw<float>::store(part + col, an[j]);
-    if (post) Raw<float>::store(part + H + col, ap[j]);
-    if (kind == GATE_COLUMN) Raw<float>::store(part + 2 * (size_t)H + col, ag[j]);
+    const auto put = [&](float* to, const float* f) {   // read back at once
+      *(float4*)to = make_float4(f[0], f[1], f[2], f[3]);
+      *(float4*)(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    };
+    if (next) put(part + col, an[j]);
+    if (post) put(part + H + col, ap[j]);
+    if (kind == GATE_COLUMN) put(part + 2 * (size_t)H + col, ag[j]);
   }
 }
 
@@ -300,10 +309,13 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(ReduceArgs p) {
   if (!out) return;
   const int c = blockIdx.x * 64 + (threadIdx.x & 63), g = threadIdx.x >> 6;
   float v = 0.f;
-  if (c < p.H) {
+  if (c < p.H && p.rows > 0) {   // all loads in flight; rows past the last read the last one
     const float* a = p.part + (size_t)blockIdx.y * p.H + c;
-#pragma unroll 8
-    for (int r = g; r < p.rows; r += 16) v += a[(size_t)r * 3 * p.H];
+    float t[NORM_GRID / 16];
+#pragma unroll
+    for (int i = 0; i < NORM_GRID / 16; ++i) t[i] = a[(size_t)min(g + 16 * i, p.rows - 1) * 3 * p.H];
+#pragma unroll
+    for (int i = 0; i < NORM_GRID / 16; ++i) v += g + 16 * i < p.rows ? t[i] : 0.f;
   }
   red[g][threadIdx.x & 63] = v;
   __syncthreads();
