@@ -4,7 +4,7 @@
 
 namespace moe {
 
-constexpr int ORTHO_PARTS = 64;   // most partial sums of a matrix's squares
+constexpr int ORTHO_PARTS = 256;   // most partial sums of a matrix's squares
 
 // Iterates X and Gram matrices are kept in fp16 with these factors.
 constexpr float ORTHO_X = 64.f, ORTHO_P = 4096.f;

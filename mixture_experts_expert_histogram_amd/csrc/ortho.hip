@@ -57,6 +57,15 @@ __device__ __forceinline__ void load8(const void* p, size_t i, float* v) {
   }
 }
 
+// The sum of every thread's value, in a fixed order, in every thread.
+__device__ __forceinline__ double sum_256(double v, double (&red)[4]) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return red[0] + red[1] + red[2] + red[3];
+}
+
 // The update's squares, summed by workgroup, and a step's new momentum: one
 // pass over g (and m), bound by HBM.
 template <bool F32>
@@ -81,19 +90,17 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum += (double)u[e] * u[e];
   }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) p.part[blockIdx.y * ORTHO_PARTS + blockIdx.x] = red[0] + red[1] + red[2] + red[3];
+  sum = sum_256(sum, red);
+  if (threadIdx.x == 0) p.part[blockIdx.y * ORTHO_PARTS + blockIdx.x] = sum;
 }
 
 // X = u / (|u| + eps) in fp16, times ORTHO_X; a step's u again from g and m'.
 template <bool F32>
 __global__ __launch_bounds__(256) void ortho_scale_kernel(OrthoArgs p, int parts) {
+  static_assert(ORTHO_PARTS <= 256, "a partial sum a thread");
+  __shared__ double red[4];
   const size_t n = (size_t)p.M * p.N, at = n * blockIdx.y;
-  double sum = 0.0;
-  for (int i = 0; i < parts; ++i) sum += p.part[blockIdx.y * ORTHO_PARTS + i];
+  const double sum = sum_256((int)threadIdx.x < parts ? p.part[blockIdx.y * ORTHO_PARTS + threadIdx.x] : 0.0, red);
   const float f = (float)(ORTHO_X / (sqrt(sum) + (double)p.eps));
   for (size_t i = (blockIdx.x * 256ul + threadIdx.x) * 8; i < n; i += gridDim.x * 2048ul) {
     float u[8];
@@ -350,8 +357,9 @@ using namespace dense;
 
 hipError_t launch_ortho(const OrthoArgs& p, hipStream_t s) {
   const size_t n = (size_t)p.M * p.N;
-  const size_t want = (n + 8191) / 8192;   // 4 groups of 8 elements a thread, or more
-  const int parts = (int)(want < ORTHO_PARTS ? want : ORTHO_PARTS);
+  // workgroups of a matrix: 4 groups of 8 elements a thread, or more where that makes over 4096 in all
+  const size_t want = (n + 8191) / 8192, most = 4096 / p.E < 16 ? 16 : 4096 / p.E < ORTHO_PARTS ? 4096 / p.E : ORTHO_PARTS;
+  const int parts = (int)(want < most ? want : most);
   hipError_t e = run_kernel("ortho_norm", s, [&] {
     if (p.g_f32) ortho_norm_kernel<true><<<dim3(parts, p.E), 256, 0, s>>>(p);
     else ortho_norm_kernel<false><<<dim3(parts, p.E), 256, 0, s>>>(p);
