@@ -432,9 +432,9 @@ moe_status_t moe_residual_bwd(const moe_norm_desc_t* desc, const void* x_new,
  * Iterates are fp16 (11 bits) with fp32 sums, so X is about 1e-3 from the
  * exact iteration in the 2-norm before it is rounded to its type; the norm is
  * summed in 64 bits.  Coefficients must keep the iterates' singular values,
- * which start at most 1, at most 3 and b x + c x^2 at most 14.6 in size over
- * their squares (checked; the usual 3.4445, -4.775, 2.0315 reach 1.21 and
- * 2.81), else MOE_ERR_UNSUPPORTED.  A NaN or infinity makes its matrix's X
+ * which start at most 1, at most 3 and b x + c x^2 and a + b x + c x^2 at most
+ * 14.6 in size over their squares (checked; the usual 3.4445, -4.775, 2.0315
+ * reach 1.21, 2.81 and 3.45), else MOE_ERR_UNSUPPORTED.  A NaN or infinity makes its matrix's X
  * NaN; a zero matrix stays zero.
  * M and N multiples of 8, at most 2^20, E at most 65535, 1 to 64 steps, else
  * MOE_ERR_UNSUPPORTED (negative E, M or N, M or N of 0, eps or dtypes that do

@@ -127,8 +127,8 @@ struct OrthoLayout {
   size_t part, x0, x1, p, q, end;
 };
 
-// Largest sizes of the iterates' singular values, and of b x + c x^2 over
-// their squares, must leave the fp16 iterates room.  Singular values start at
+// Largest sizes of the iterates' singular values, and of b x + c x^2 and a + b x
+// + c x^2 over their squares, must leave the fp16 iterates room.  Singular values start at
 // most 1; the polynomial's range over the present interval is the next one.
 bool coefficients_ok(const moe_ortho_desc_t* d) {
   double top = 1.001;
@@ -137,7 +137,8 @@ bool coefficients_ok(const moe_ortho_desc_t* d) {
     for (int k = 0; k <= 4096; ++k) {
       const double s = top * k / 4096, x = s * s;
       next = fmax(next, fabs(s * (d->a + x * (d->b + x * (double)d->c))));
-      q = fmax(q, fabs(x * (d->b + x * (double)d->c)));
+      const double r = x * (d->b + x * (double)d->c);
+      q = fmax(q, fmax(fabs(r), fabs(d->a + r)));
       if (!(fabs(s * (d->a + x * (d->b + x * (double)d->c))) < 1e30)) return false;   // NaN too
     }
     if (!(top <= 3.0) || !(q <= 14.6)) return false;

@@ -1,4 +1,4 @@
-// The choice of the dense products' tiles, and their launches.
+// Pieces of the dense products' epilogues, and the choice of their tiles.
 #pragma once
 #include <type_traits>
 #include <utility>
@@ -7,6 +7,15 @@
 
 namespace moe {
 namespace dense {
+
+// Four fp32 values each of two 4-column groups (columns c .. and c + 8 .. of a
+// row, c = 4 (lane / 32)) as bf16, so that every lane ends with 8 consecutive
+// columns: lanes below 32 columns 0 .. 7, the others 8 .. 15 of the 16.
+__device__ __forceinline__ u32x4 pack_pair(const float* lo, const float* hi) {
+  const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16(lo[0], lo[1]), pack_bf16(hi[0], hi[1]), false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(pack_bf16(lo[2], lo[3]), pack_bf16(hi[2], hi[3]), false, false);
+  return u32x4{a[0], b[0], a[1], b[1]};
+}
 
 // A wave's FM x FN result fragments in turn, use(i, j, r) with what fetch(i, j,
 // r) loaded for each DEPTH fragments earlier, so that an epilogue waits for

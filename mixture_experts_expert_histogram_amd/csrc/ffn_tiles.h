@@ -6,15 +6,6 @@
 namespace moe {
 namespace dense {
 
-// Four fp32 values each of two 4-column groups (columns c .. and c + 8 .. of a
-// row, c = 4 (lane / 32)) as bf16, so that every lane ends with 8 consecutive
-// columns: lanes below 32 columns 0 .. 7, the others 8 .. 15 of the 16.
-__device__ __forceinline__ u32x4 pack_pair(const float* lo, const float* hi) {
-  const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16(lo[0], lo[1]), pack_bf16(hi[0], hi[1]), false, false);
-  const auto b = __builtin_amdgcn_permlane32_swap(pack_bf16(lo[2], lo[3]), pack_bf16(hi[2], hi[3]), false, false);
-  return u32x4{a[0], b[0], a[1], b[1]};
-}
-
 // Block of 32 rows x 8 columns of the saved gate (up = 0) and up values: 256
 // floats, lane l's four at 4 l, the order in which the accumulators hold them,
 // so that both passes move whole kilobytes.

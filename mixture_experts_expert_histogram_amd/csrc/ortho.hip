@@ -3,8 +3,8 @@
 //
 //   m' = mu m + g,  u = g + mu m' (Nesterov) or m'   (a step; otherwise u = g)
 //   X = u / (|u| + eps)                                (2-norm of all elements)
-//   `steps` times:  P = X X^T,  Q = b P + c P P,  X <- a X + Q X
-//                   (matrices with more rows than columns: P = X^T X, X <- a X + X Q)
+//   `steps` times:  P = X X^T,  Q = a I + b P + c P P,  X <- Q X
+//                   (matrices with more rows than columns: P = X^T X, X <- X Q)
 //   w' = (1 - decay) w - lr X                          (a step; otherwise out = X)
 //
 // The products are bound by the matrix cores.  P and Q are symmetric, so only
@@ -16,8 +16,10 @@
 // X, P and Q are held in fp16, which the singular values' known range allows
 // (at most 1.21 with the usual coefficients; the host checks others): 11
 // significant bits where bf16 has 8, at the same matrix rate.  With a bf16
-// result the whole is 2.1e-3 from 64 bits in the 2-norm, of which the result's
-// rounding is 1.66e-3; with bf16 iterates it would be 1.1e-2.  Factors 2^6 on X
+// result the whole is 2.0e-3 from 64 bits in the 2-norm, of which the result's
+// rounding is 1.66e-3; with bf16 iterates it would be 1.1e-2.  a X as a I within
+// Q costs no accuracy (its rounding is one of 11 bits on the diagonal) and
+// leaves the update a plain product, whose epilogue reads nothing.  Factors 2^6 on X
 // and 2^12 on P and Q keep small elements out of the subnormal range.  Sums and
 // the polynomial's terms are fp32, the norm is summed in 64 bits (no overflow
 // or underflow of fp32 gradients' squares).
@@ -35,7 +37,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const f16x2_t v = {(_Float16)lo, (_Float16)hi};
   return __builtin_bit_cast(uint32_t, v);
 }
-// As pack_pair (ffn_tiles.h), to fp16.
+// As pack_pair, to fp16.
 __device__ __forceinline__ u32x4 pack_pair_f16(const float* lo, const float* hi) {
   const auto a = __builtin_amdgcn_permlane32_swap(pack_f16(lo[0], lo[1]), pack_f16(hi[0], hi[1]), false, false);
   const auto b = __builtin_amdgcn_permlane32_swap(pack_f16(lo[2], lo[3]), pack_f16(hi[2], hi[3]), false, false);
@@ -119,14 +121,14 @@ __global__ __launch_bounds__(256) void ortho_scale_kernel(OrthoArgs p, int parts
 // ------------------------------------------------------------------ symmetric products
 struct SymArgs {
   const uint16_t* a;   // [E] matrices: rows of K (ROWS), or K rows of S
-  const uint16_t* p;   // QUAD: [E,S,S], the P of b P + c P P
+  const uint16_t* p;   // QUAD: [E,S,S], P
   uint16_t* out;       // [E,S,S]
   size_t a_step;       // elements of a matrix of a
   int E, S, K, tiles;  // tiles: of a side
-  float b, c;
+  float a_diag, b, c;  // QUAD: a_diag I + b P + c A A^T
 };
 
-// out = A A^T (QUAD: b P + c A A^T) for square tiles on and above the diagonal,
+// out = A A^T (QUAD: a_diag I + b P + c A A^T) for square tiles on and above the diagonal,
 // each stored where it belongs and, mirrored, below.  The mirror goes through
 // LDS: the tile is written there as it lies in the registers and read back with
 // the transposing reads.  COLS: A is held as its transpose (K rows of S).
@@ -183,6 +185,7 @@ __global__ __launch_bounds__(256, 1) void ortho_sym_kernel(SymArgs p) {
             for (int k = 0; k < 4; ++k) {
               const float s = acc[i][j][8 * q + 4 * h + k];
               v[h][k] = QUAD ? p.b * (float)held.v[2 * q + h][k] + p.c * s : s;
+              if (QUAD && mt == nt && tr == tc + 8 * h + c4 + k) v[h][k] += p.a_diag;
             }
             if (mt != nt) {
               const int ct = tc + 8 * h;
@@ -216,14 +219,14 @@ __global__ __launch_bounds__(256, 1) void ortho_sym_kernel(SymArgs p) {
   }
 }
 
-// ------------------------------------------------------------------ X <- a X + Q X (or X Q)
+// ------------------------------------------------------------------ X <- Q X (or X Q)
 enum { TO_X = 0, TO_BF16 = 1, TO_F32 = 2 };
 struct UpdateArgs {
   const uint16_t *x, *q;
   void* out;
   const void* w;   // the weights that a step updates, or null
   int E, M, N, S, mt, nt;
-  float a, lr, keep;
+  float lr, keep;
 };
 __device__ __forceinline__ void load4(const uint16_t* p, float* v) {
   const uint2 w = *(const uint2*)p;
@@ -263,21 +266,17 @@ __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
     rows(bs, Q, n0, S);
     mainloop<C, f16x8_t>(as, bs, S, lds, acc, wave, lane);
   }
-  // the products carry ORTHO_X ORTHO_P, x ORTHO_X
-  const float fx = TO == TO_X ? p.a : p.a / ORTHO_X, fs = TO == TO_X ? 1.f / ORTHO_P : 1.f / (ORTHO_X * ORTHO_P);
+  const float f = TO == TO_X ? 1.f / ORTHO_P : 1.f / (ORTHO_X * ORTHO_P);   // the products carry ORTHO_X ORTHO_P
   const size_t at = (size_t)M * N * e;
   const int r0 = m0 + wm * 32 * C::FM + (lane & 31), c00 = n0 + wn * 32 * C::FN, c4 = 4 * (lane >> 5);
   const bool step = TO != TO_X && p.w != nullptr;
-  struct Held { f16x4_t x[4]; float w[TO == TO_X ? 1 : 4][4]; };
-  each_fragment<C, Held, (TO == TO_X ? 4 : 2)>(
+  struct Held { float w[4][4]; };
+  each_fragment<C, Held, 2>(
       [&](int i, int j, Held& h) __attribute__((always_inline)) {   // rows and columns past the last read the last one
-        const size_t row = (size_t)min(r0 + 32 * i, M - 1) * N;
+        if (!step) return;
+        const size_t row = at + (size_t)min(r0 + 32 * i, M - 1) * N;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const size_t el = row + min(c00 + 32 * j + 8 * v, N - 8) + c4;
-          h.x[v] = *(const f16x4_t*)(X + el);
-          if (TO != TO_X && step) load4((const T*)p.w + at + el, h.w[v]);
-        }
+        for (int v = 0; v < 4; ++v) load4((const T*)p.w + row + min(c00 + 32 * j + 8 * v, N - 8) + c4, h.w[v]);
       },
       [&](int i, int j, const Held& held) __attribute__((always_inline)) {
         const int row = r0 + 32 * i;
@@ -289,8 +288,8 @@ __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float o = fx * (float)held.x[2 * q + h][k] + fs * acc[i][j][8 * q + 4 * h + k];
-              v[h][k] = step ? p.keep * held.w[TO == TO_X ? 0 : 2 * q + h][k] - p.lr * o : o;
+              const float o = f * acc[i][j][8 * q + 4 * h + k];
+              v[h][k] = step ? p.keep * held.w[2 * q + h][k] - p.lr * o : o;
             }
           if constexpr (TO == TO_F32) {
 #pragma unroll
@@ -298,14 +297,7 @@ __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
               if (row < M && c + 8 * h < N)
                 store4<float>((float*)p.out + at + (size_t)row * N + c + 8 * h + c4, v[h][0], v[h][1], v[h][2], v[h][3]);
           } else {
-            u32x4 o;
-            if constexpr (TO == TO_X) {
-              o = pack_pair_f16(v[0], v[1]);
-            } else {
-              const auto a = __builtin_amdgcn_permlane32_swap(pack_bf16(v[0][0], v[0][1]), pack_bf16(v[1][0], v[1][1]), false, false);
-              const auto b = __builtin_amdgcn_permlane32_swap(pack_bf16(v[0][2], v[0][3]), pack_bf16(v[1][2], v[1][3]), false, false);
-              o = u32x4{a[0], b[0], a[1], b[1]};
-            }
+            const u32x4 o = TO == TO_X ? pack_pair_f16(v[0], v[1]) : pack_pair(v[0], v[1]);
             const int cc = c + 2 * c4;
             if (row < M && cc < N) *(u32x4*)((uint16_t*)p.out + at + (size_t)row * N + cc) = o;
           }
@@ -375,10 +367,10 @@ hipError_t launch_ortho(const OrthoArgs& p, hipStream_t s) {
   for (int i = 0; i < p.steps && e == hipSuccess; ++i) {
     const bool last = i + 1 == p.steps;
     // X X^T carries ORTHO_X^2 = ORTHO_P; P P carries ORTHO_P^2
-    e = sym({x, nullptr, P, n, p.E, p.S, wide ? p.N : p.M, 0, 0.f, 1.f}, !wide, false, s);
-    if (e == hipSuccess) e = sym({P, P, Q, ss, p.E, p.S, p.S, 0, p.b, p.c / ORTHO_P}, false, true, s);
+    e = sym({x, nullptr, P, n, p.E, p.S, wide ? p.N : p.M, 0, 0.f, 0.f, 1.f}, !wide, false, s);
+    if (e == hipSuccess) e = sym({P, P, Q, ss, p.E, p.S, p.S, 0, ORTHO_P * p.a, p.b, p.c / ORTHO_P}, false, true, s);
     if (e == hipSuccess)
-      e = update({x, Q, last ? p.out : y, last ? p.w : nullptr, p.E, p.M, p.N, p.S, 0, 0, p.a, p.lr, p.keep},
+      e = update({x, Q, last ? p.out : y, last ? p.w : nullptr, p.E, p.M, p.N, p.S, 0, 0, p.lr, p.keep},
                  !last ? TO_X : p.out_f32 ? TO_F32 : TO_BF16, s);
     uint16_t* t = x;
     x = y;

@@ -148,8 +148,8 @@ def column_sum(terms, err):
 
 # ------------------------------------------------------------------ Newton-Schulz
 def newton_schulz(u, coef, steps, eps, half=False):
-    """The iteration in 64 bits; half: with X, X X^T and Q rounded to fp16 (scaled by 2^6 and 2^12) as the kernels hold
-    them, for the size of the error that this brings."""
+    """The iteration in 64 bits; half: with X, X X^T and Q = a I + b X X^T + .. rounded to fp16 (scaled by 2^6 and 2^12)
+    as the kernels hold them, for the size of the error that this brings."""
     a, b, c = coef
     x = u.double() / (u.double().square().sum((-2, -1), keepdim=True).sqrt() + eps)
     flip = x.shape[-2] > x.shape[-1]
@@ -161,8 +161,7 @@ def newton_schulz(u, coef, steps, eps, half=False):
     x = hold(x, 64.0)
     for i in range(steps):
         p = hold(x @ x.mT.contiguous(), 4096.0)
-        q = hold(b * p + c * (p @ p), 4096.0)
-        x = a * x + q @ x
+        x = hold(a * torch.eye(p.shape[-1], dtype=p.dtype, device=p.device) + b * p + c * (p @ p), 4096.0) @ x
         if i + 1 < steps:
             x = hold(x, 64.0)
     return x.mT.contiguous() if flip else x
