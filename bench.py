@@ -450,6 +450,66 @@ def separate_record(runner, warmup, iters):
             "tflops": round(flops / (t_sep * 1e-3) / 1e12, 2), "fused_median_ms": round(t_fused, 4)}
 
 
+def block_record(runner, warmup, iters):
+    """The block around the layer, forward and backward, each iteration after the cache flush: norm, routed experts beside a
+    shared expert of the same size (added to their output by a gate for each token), the residual step with a post-norm and
+    the next block's norm.  `layer` is the routed experts' part alone; `orthogonalised_step` an optimiser step of 16
+    experts' gate_up and down weights on their gradients."""
+    import numpy as np
+    import torch
+    import mixture_experts_expert_histogram_amd as moe
+    wl, dev, dt = runner.wl, runner.X.device, runner.X.dtype
+    T, H, I = wl.T, wl.H, wl.I
+    g = torch.Generator(device=dev).manual_seed(1)
+
+    def rand(*shape, std=1.0):
+        return torch.empty(shape, device=dev, dtype=torch.float32).normal_(0, std, generator=g)
+    gu, dn = rand(2 * I, H, std=0.02).to(dt), rand(H, I, std=0.02).to(dt)
+    w_in, w_post, w_next = (torch.ones(H, dtype=dt, device=dev) for _ in range(3))
+    gate, x = rand(T), rand(T, H).to(dt)
+    d_new, d_y = rand(T, H, std=0.1).to(dt), rand(T, H, std=0.1).to(dt)
+    kw = dict(act=wl.act, layout=wl.layout)
+    lkw = dict(limit=wl.limit, alpha=wl.alpha, **kw)
+    back = {}
+
+    def forward():
+        y = moe.norm_fwd(x, w_in)
+        moe.fwd(y, runner.ids, runner.w, runner.Wgu, runner.Wd, save=True, ws=runner.ws_f, out=runner.out,
+                saved=runner.saved, **lkw)
+        h, saved, _ = moe.ffn_fwd(y, gu, dn, gate=gate, add=runner.out, save=True, **kw)
+        new, _ = moe.residual_fwd(x, h, w_post=w_post, w_next=w_next)
+        back.update(y=y, h=h, saved=saved, new=new)
+
+    def backward():
+        r = moe.residual_bwd(back["new"], back["h"], d_new, d_y, w_post=w_post, w_next=w_next)
+        dx, *_ = moe.ffn_bwd(back["y"], gu, dn, r.d_h, saved=back["saved"], gate=gate, **kw)
+        moe.bwd(back["y"], runner.ids, runner.w, runner.Wgu, runner.Wd, r.d_h, saved=runner.saved, ws=runner.ws_b,
+                grads=runner.grads, grad_dtype=runner.grad_dtype, **lkw)
+        moe.norm_bwd(x, w_in, dx.add_(runner.grads[0]), d_add=r.d_x)
+
+    n = min(16, wl.E)
+    m = [torch.zeros(w[:n].shape, dtype=torch.float32, device=dev) for w in (runner.Wgu, runner.Wd)]
+
+    def update():   # into new weights: the runner's stay as they are
+        for w, grad, mom in zip((runner.Wgu, runner.Wd), runner.grads[2:], m):
+            moe.muon_step(w[:n], grad[:n], mom, lr=0.02, out=(torch.empty_like(w[:n]), mom))
+
+    def layer():
+        runner.fwd(True)
+        runner.bwd(True)
+
+    def both():
+        forward()
+        backward()
+
+    def ms(f):
+        return round(float(np.median(runner.time(f, warmup, iters))), 4)
+    times = {"block_median_ms": ms(both), "forward_median_ms": ms(forward), "backward_median_ms": ms(backward),
+             "layer_median_ms": ms(layer), "orthogonalised_step_median_ms": ms(update)}
+    return {"workload": wl.name, "pass": "block fwd+bwd", "T": T, "H": H, "I": I, "E": wl.E, "K": wl.K,
+            "orthogonalised_experts": n, **times}
+
+
 def run_protocol(args):
     import torch
     from synth import WORKLOADS
@@ -459,6 +519,7 @@ def run_protocol(args):
         print(json.dumps(router_record(WORKLOADS[name], dev, args.warmup, args.iters)), flush=True)
     runner = PassRunner(WORKLOADS["gptoss"], dev, grad_dtype=args.grad_dtype)
     print(json.dumps(separate_record(runner, args.warmup, args.iters)), flush=True)
+    print(json.dumps(block_record(runner, args.warmup, args.iters)), flush=True)
     print(json.dumps(oracle_record(WORKLOADS["tiny"], None, 0)), flush=True)
     current, runner = None, None
     for name, pass_, saved in PROTOCOL:
