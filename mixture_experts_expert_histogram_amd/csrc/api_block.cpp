@@ -127,21 +127,29 @@ struct OrthoLayout {
   size_t part, x0, x1, p, q, end;
 };
 
-// Largest sizes of the iterates' singular values, and of b x + c x^2 and a + b x
-// + c x^2 over their squares, must leave the fp16 iterates room.  Singular values start at
-// most 1; the polynomial's range over the present interval is the next one.
+// Largest sizes of the iterates' singular values s, and of b x + c x^2 and a + b
+// x + c x^2 over their squares x, must leave the fp16 iterates room.  Singular
+// values start at most 1; the largest |s (a + b x + c x^2)| over the present
+// interval is the next one's end.  Extremes of a polynomial over [0, top]: at
+// the end or where the derivative, here at most quadratic in x, is zero.
 bool coefficients_ok(const moe_ortho_desc_t* d) {
+  const double a = d->a, b = d->b, c = d->c;
+  const double disc = 9 * b * b - 20 * a * c, root = disc >= 0 ? sqrt(disc) : 0;
+  const double places[] = {(-3 * b + root) / (10 * c), (-3 * b - root) / (10 * c), -a / (3 * b), -b / (2 * c)};
   double top = 1.001;
   for (int i = 0; i < d->steps; ++i) {
+    const double end = top * top;
     double next = 0, q = 0;
-    for (int k = 0; k <= 4096; ++k) {
-      const double s = top * k / 4096, x = s * s;
-      next = fmax(next, fabs(s * (d->a + x * (d->b + x * (double)d->c))));
-      const double r = x * (d->b + x * (double)d->c);
-      q = fmax(q, fmax(fabs(r), fabs(d->a + r)));
-      if (!(fabs(s * (d->a + x * (d->b + x * (double)d->c))) < 1e30)) return false;   // NaN too
-    }
-    if (!(top <= 3.0) || !(q <= 14.6)) return false;
+    const auto at = [&](double x) {
+      const double r = x * (b + x * c);
+      next = fmax(next, sqrt(x) * fabs(a + r));
+      q = fmax(q, fmax(fabs(r), fabs(a + r)));
+    };
+    at(0);
+    at(end);
+    for (double x : places)
+      if (x > 0 && x < end) at(x);   // not where a coefficient is zero (infinite or NaN)
+    if (!isfinite(a) || !isfinite(b) || !isfinite(c) || !(top <= 3.0) || !(q <= 14.6)) return false;
     top = 1.001 * next;
   }
   return true;
