@@ -103,7 +103,9 @@ __global__ __launch_bounds__(256) void ortho_scale_kernel(OrthoArgs p, int parts
   __shared__ double red[4];
   const size_t n = (size_t)p.M * p.N, at = n * blockIdx.y;
   const double sum = sum_256((int)threadIdx.x < parts ? p.part[blockIdx.y * ORTHO_PARTS + threadIdx.x] : 0.0, red);
-  const float f = (float)(ORTHO_X / (sqrt(sum) + (double)p.eps));
+  // in two factors, whose product may be past fp32's range (eps of 0 and subnormal updates)
+  const double whole = ORTHO_X / (sqrt(sum) + (double)p.eps), part = fmin(whole, 0x1p100);
+  const float f = sum == 0.0 ? 0.f : (float)part, f2 = sum == 0.0 ? 0.f : (float)(whole / part);
   for (size_t i = (blockIdx.x * 256ul + threadIdx.x) * 8; i < n; i += gridDim.x * 2048ul) {
     float u[8];
     load8<F32>(p.g, at + i, u);
@@ -113,8 +115,10 @@ __global__ __launch_bounds__(256) void ortho_scale_kernel(OrthoArgs p, int parts
 #pragma unroll
       for (int e = 0; e < 8; ++e) u[e] = p.nesterov ? u[e] + p.momentum * m[e] : m[e];
     }
-    *(uint4*)((uint16_t*)p.x0 + at + i) = make_uint4(pack_f16(u[0] * f, u[1] * f), pack_f16(u[2] * f, u[3] * f),
-                                                    pack_f16(u[4] * f, u[5] * f), pack_f16(u[6] * f, u[7] * f));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] *= f, u[e] *= f2;
+    *(uint4*)((uint16_t*)p.x0 + at + i) = make_uint4(pack_f16(u[0], u[1]), pack_f16(u[2], u[3]), pack_f16(u[4], u[5]),
+                                                    pack_f16(u[6], u[7]));
   }
 }
 

@@ -146,3 +146,16 @@ def test_empty_stack_and_leading_dimensions():
     b, _ = moe.orthogonalize(u.view(2, 3, 40, 24))
     c, _ = moe.orthogonalize(u[4])
     assert torch.equal(b.view(6, 40, 24), a) and torch.equal(c, a[4])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_eps_of_zero(dtype):
+    """Zero matrices stay zero, and subnormal ones, whose norm's reciprocal is past fp32's range, are orthogonalised."""
+    u = updates(5, 64, 136, dtype, std=1.0)
+    u[0] *= 2.0 ** -130
+    u[2] = 0
+    u[3] *= 2.0 ** 100
+    o, _ = moe.orthogonalize(u, eps=0.0)
+    assert torch.count_nonzero(o[2]) == 0
+    keep = [0, 1, 3, 4]
+    compare(o[keep], u[keep], eps=0.0)
