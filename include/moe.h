@@ -334,7 +334,8 @@ moe_status_t moe_mx_fwd_logits(const moe_desc_t* desc, const void* hidden,
  * (else MOE_ERR_INVALID_ARG).  x, out, add [T,H]; w_gate_up [2I,H]; w_down
  * [H,I]; gate fp32 [T].  add may be NULL (zero) and may be out; gate may be
  * NULL (s = 1).
- *   - H and I at most 2^20 and H I at most 2^28, else MOE_ERR_UNSUPPORTED.
+ *   - H and I at most 2^20, H I at most 2^28, T at most 2^30 and at most 2^23
+ *     tiles of 256 x 256 in [T, max(2I, H)], else MOE_ERR_UNSUPPORTED.
  *   - a = phi(..) is rounded to the activations' type as the second product's
  *     operand; sums are fp32; out is rounded once.
  *   - Up to 16 tokens (bf16) or 64 (fp32) without `saved` run on kernels that
@@ -383,7 +384,8 @@ moe_status_t moe_ffn_bwd(const moe_desc_t* desc, const void* x,
  * NULL is allowed for d_add and d_x_new (zero), w_post and w_next (no such
  * norm; its gradient's pointer is then ignored, as d_y is without w_next), and
  * gate with MOE_GATE_NONE.  x_new may be x, and d_x may be d_add or d_x_new.
- * H a multiple of 8, at most 16384, else MOE_ERR_UNSUPPORTED; T < 2^31.
+ * H a multiple of 8, at most 16384, and T at most 2^30, else
+ * MOE_ERR_UNSUPPORTED.  With an eps of 0 a row of zeros has no rms and is NaN.
  * T = 0 writes zeros to the weights' (and a column gate's) gradients.
  * ws (backward): moe_norm_workspace_size() bytes.  Deterministic. */
 typedef enum {
@@ -434,10 +436,10 @@ moe_status_t moe_residual_bwd(const moe_norm_desc_t* desc, const void* x_new,
  * summed in 64 bits.  Coefficients must keep the iterates' singular values,
  * which start at most 1, at most 3 and b x + c x^2 and a + b x + c x^2 at most
  * 14.6 in size over their squares (checked; the usual 3.4445, -4.775, 2.0315
- * reach 1.21, 2.81 and 3.45), else MOE_ERR_UNSUPPORTED.  A NaN or infinity makes its matrix's X
- * NaN; a zero matrix stays zero.
- * M and N multiples of 8, at most 2^20, E at most 65535, 1 to 64 steps, else
- * MOE_ERR_UNSUPPORTED (negative E, M or N, M or N of 0, eps or dtypes that do
+ * reach 1.21, 2.81 and 3.45), else MOE_ERR_UNSUPPORTED.  A NaN or infinity
+ * makes its matrix's X NaN; a zero matrix stays zero, with an eps of 0 too.
+ * M and N multiples of 8, at most 2^20, E at most 65535, at most 2^23 tiles of
+ * 256 x 256 in all the matrices, 1 to 64 steps, else MOE_ERR_UNSUPPORTED (negative E, M or N, M or N of 0, eps or dtypes that do
  * not exist: MOE_ERR_INVALID_ARG).  E = 0 does nothing. */
 typedef struct {
   int64_t E, M, N;

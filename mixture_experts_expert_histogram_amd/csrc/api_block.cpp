@@ -16,6 +16,9 @@ namespace {
 
 constexpr int64_t kMaxSide = int64_t(1) << 20;   // 32-bit offsets within a tile's rows
 
+// Tiles of the largest kind, 256 x 256.
+inline int64_t tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256); }
+
 inline size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Every pointer present (where `need`) and 16-byte aligned.
@@ -52,8 +55,7 @@ moe_status_t ffn_check(const moe_desc_t* d, FfnLayout* L) {
   if (st != MOE_OK) return st;
   if (d->E != 1 || d->K != 1) return MOE_ERR_INVALID_ARG;
   if (d->H > kMaxSide || d->I > kMaxSide || d->H * d->I > (int64_t(1) << 28)) return MOE_ERR_UNSUPPORTED;
-  // workgroups of the smallest tiles
-  if (((d->T + 63) / 64 + 8) * ((2 * d->I + d->H) / 64 + 8) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (d->T > (int64_t(1) << 30) || tiles(d->T, 2 * d->I > d->H ? 2 * d->I : d->H) > MAX_TILES) return MOE_ERR_UNSUPPORTED;
   const size_t esz = d->dtype == MOE_BF16 ? 2 : 4, T = (size_t)d->T, I = (size_t)d->I;
   *L = {};
   L->one_expert = d->dtype == MOE_F32;
@@ -109,7 +111,7 @@ moe_status_t norm_check(const moe_norm_desc_t* d) {
   if (!d || d->T < 0 || d->H < 1 || !dtype_ok(d->dtype) || d->gate_kind < MOE_GATE_NONE || d->gate_kind > MOE_GATE_FULL ||
       !(d->eps >= 0.f))
     return MOE_ERR_INVALID_ARG;
-  if (d->H % 8 != 0 || d->H > NORM_MAX_H || d->T >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (d->H % 8 != 0 || d->H > NORM_MAX_H || d->T > NORM_MAX_T) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 size_t norm_ws(const moe_norm_desc_t* d) {
@@ -160,7 +162,7 @@ moe_status_t ortho_check(const moe_ortho_desc_t* d, OrthoLayout* L) {
     return MOE_ERR_INVALID_ARG;
   if (d->M % 8 != 0 || d->N % 8 != 0 || d->M > kMaxSide || d->N > kMaxSide || d->E > 65535 || d->steps < 1 || d->steps > 64)
     return MOE_ERR_UNSUPPORTED;
-  if (d->E * (d->M / 64 + 1) * (d->N / 64 + 1) >= (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;
+  if (d->E * tiles(d->M, d->N) > MAX_TILES) return MOE_ERR_UNSUPPORTED;
   if (!coefficients_ok(d)) return MOE_ERR_UNSUPPORTED;
   const size_t S = (size_t)(d->M < d->N ? d->M : d->N), E = (size_t)d->E;
   L->part = 0;

@@ -298,7 +298,9 @@ PyObject* ffn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* add = input(a[8], "add", x.sizes(), x.scalar_type(), dev);
     const Tensor ws = workspace(a[10], f.fwd, dev), out = output(a[11], "out", x.sizes(), x.scalar_type(), dev);
     std::optional<Tensor> saved;
-    if (PyObject_IsTrue(a[9])) saved = workspace(a[12], f.saved, dev);
+    const int save = PyObject_IsTrue(a[9]);
+    if (save < 0) throw PythonError{};
+    if (save) saved = workspace(a[12], f.saved, dev);
     launch(dev, "moe_ffn_fwd", [&](hipStream_t s) {
       return moe_ffn_fwd(&f.d, data(x), data(gu), data(dn), gate_of(a[3]), add, data(out), saved ? data(*saved) : nullptr,
                          saved ? saved->nbytes() : 0, data(ws), ws.nbytes(), s);

@@ -66,14 +66,15 @@ inline float tile_time(const TileKind& k, long tiles, long K) {
 }
 
 // The kind of tile that an M x N product over K, `batch` times, is done with
-// soonest.
+// soonest, of those whose tiles a launch holds (the host checks the largest kind).
 inline int tile_kind(long M, long N, long K, long batch = 1) {
   int best = 0;
   float least = 0.f;
   for (int i = 0; i < N_TILES; ++i) {
     const TileKind& k = kTiles[i];
-    const float t = tile_time(k, batch * ((M + 64 * k.fm - 1) / (64 * k.fm)) * ((N + 64 * k.fn - 1) / (64 * k.fn)), K);
-    if (i == 0 || t < least) best = i, least = t;
+    const long tiles = batch * ((M + 64 * k.fm - 1) / (64 * k.fm)) * ((N + 64 * k.fn - 1) / (64 * k.fn));
+    const float t = tile_time(k, tiles, K);
+    if (i == 0 || (t < least && tiles <= MAX_TILES)) best = i, least = t;
   }
   return best;
 }
@@ -99,9 +100,9 @@ inline int square_tile_kind(long S, long K, long batch) {
   for (int i = 0; i < N_TILES; ++i) {
     const TileKind& k = kTiles[i];
     if (k.fm != k.fn) continue;
-    const long side = (S + 64 * k.fm - 1) / (64 * k.fm);
-    const float t = tile_time(k, batch * side * (side + 1) / 2, K);
-    if (best < 0 || t < least) best = i, least = t;
+    const long side = (S + 64 * k.fm - 1) / (64 * k.fm), tiles = batch * side * (side + 1) / 2;
+    const float t = tile_time(k, tiles, K);
+    if (best < 0 || (t < least && tiles <= MAX_TILES)) best = i, least = t;
   }
   return best;
 }

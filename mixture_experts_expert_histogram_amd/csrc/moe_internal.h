@@ -50,6 +50,9 @@ struct RouteState {
   int small_bm;           // M-tile rows of the other engine (128 or 192), for large_tile_expert
 };
 
+// Most tiles (workgroups of 256 threads) of a dense product: a launch holds fewer than 2^32 threads along x.
+constexpr int64_t MAX_TILES = int64_t(1) << 23;
+
 // Host side: optional timing events around each kernel launch (api.cpp).
 int timing_begin(const char* name, hipStream_t stream);   // slot, or -1 when not timing
 void timing_end(int slot, hipStream_t stream);

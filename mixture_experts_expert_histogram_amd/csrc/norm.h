@@ -7,6 +7,9 @@ namespace moe {
 constexpr int NORM_MAX_H = 16384;   // a row in the registers of 1024 threads
 constexpr int NORM_GRID = 512;      // most workgroups of a backward pass (partial sums of the weights' gradients)
 
+constexpr int NORM_ROWS = 1 << 21;  // most workgroups (rows) of a forward pass along x
+constexpr int64_t NORM_MAX_T = int64_t(1) << 30;
+
 struct NormArgs {
   const void* x;        // [T,H]: the residual stream before the step (forward), after it (backward)
   const void* h;        // [T,H] the block's output, or null: the norm before a block

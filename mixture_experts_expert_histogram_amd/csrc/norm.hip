@@ -110,7 +110,8 @@ template <typename T, bool H_IN>
 __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p) {
   __shared__ float red[128];
   int half = 0;
-  const size_t row = blockIdx.x;
+  const size_t row = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= (size_t)p.T) return;
   const int H = p.H;
   Raw<T> x[V], h[V], wp[V], wn[V], gt[V];
   load_row(x, (const T*)p.x, row, H);
@@ -333,9 +334,11 @@ int norm_threads(int H) { return (H / 8 + 64 * V - 1) / (64 * V) * 64; }
 template <typename T>
 hipError_t fwd(const NormArgs& p, hipStream_t s) {
   const int nt = norm_threads(p.H);
+  // a launch holds fewer than 2^32 threads along x
+  const dim3 grid(p.T < NORM_ROWS ? p.T : NORM_ROWS, (p.T + NORM_ROWS - 1) / NORM_ROWS);
   return run_kernel("norm_fwd", s, [&] {
-    if (p.h) norm_fwd_kernel<T, true><<<p.T, nt, 0, s>>>(p);
-    else norm_fwd_kernel<T, false><<<p.T, nt, 0, s>>>(p);
+    if (p.h) norm_fwd_kernel<T, true><<<grid, nt, 0, s>>>(p);
+    else norm_fwd_kernel<T, false><<<grid, nt, 0, s>>>(p);
   });
 }
 

@@ -139,3 +139,14 @@ def test_binding_refuses_host_and_odd_tensors():
               lambda: moe.orthogonalize(gu, dtype="fp16"), lambda: moe.ffn_fwd(x, gu, dn, act="relu")):
         with pytest.raises(ValueError):
             f()
+
+
+def test_more_rows_or_tiles_than_a_launch_holds():
+    for entry in (NORM_FWD, NORM_BWD):
+        assert call(entry[0], norm_desc(T=(1 << 30) + 1, H=8), entry[1], {}) == _lib.MOE_ERR_UNSUPPORTED
+    for entry in (FFN_FWD, FFN_BWD):
+        for d in (ffn_desc(T=(1 << 30) + 1, H=8, I=8), ffn_desc(T=(1 << 25) + 1, H=8, I=1 << 13), ffn_desc(T=(1 << 25) + 1, H=1 << 14, I=8)):
+            assert call(entry[0], d, entry[1], {}) == _lib.MOE_ERR_UNSUPPORTED
+    assert moe.ffn_workspace_size(ffn_desc(T=1 << 24, H=1024, I=256))[0] > 0
+    for d in (ortho_desc(E=4300, M=8, N=1 << 20), ortho_desc(E=4300, M=1 << 20, N=8)):
+        assert call(ORTHO[0], d, ORTHO[1], {}) == _lib.MOE_ERR_UNSUPPORTED

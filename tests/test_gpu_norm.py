@@ -201,3 +201,13 @@ def test_captured_and_replayed():
         assert torch.equal(new, enew) and torch.equal(y, ey)
         for a, b in zip(grads[:5], want[:5]):
             assert torch.equal(a, b)
+
+
+def test_more_rows_than_one_dimension_of_a_launch():
+    T, H = (1 << 26) + 5, 8   # 64 threads a row: over 2^32 threads
+    x = torch.randn(T, H, device="cuda", generator=torch.Generator("cuda").manual_seed(9)).bfloat16()
+    w = torch.linspace(0.5, 1.5, H, device="cuda").bfloat16()
+    y = moe.norm_fwd(x, w, out=torch.full_like(x, float("nan")))
+    for t0 in range(0, T, 1 << 24):
+        n = Norm(x[t0:t0 + (1 << 24)], w, 1e-5)
+        check(y[t0:t0 + (1 << 24)], n.n, SECOND * (n.en + half_step(torch.bfloat16) * n.n.abs()), "y")
