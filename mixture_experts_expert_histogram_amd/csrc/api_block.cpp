@@ -126,7 +126,7 @@ NormArgs norm_args(const moe_norm_desc_t* d) {
 
 // ------------------------------------------------------------ orthogonalisation
 struct OrthoLayout {
-  size_t part, x0, x1, p, q, end;
+  size_t part, x0, x1, p, q, pd, qd, end;
 };
 
 // Largest sizes of the iterates' singular values s, and of b x + c x^2 and a + b
@@ -170,7 +170,9 @@ moe_status_t ortho_check(const moe_ortho_desc_t* d, OrthoLayout* L) {
   L->x1 = L->x0 + align_up(E * d->M * d->N * 2);
   L->p = L->x1 + align_up(E * d->M * d->N * 2);
   L->q = L->p + align_up(E * S * S * 2);
-  L->end = L->q + align_up(E * S * S * 2);
+  L->pd = L->q + align_up(E * S * S * 2);
+  L->qd = L->pd + align_up(E * S * sizeof(float));
+  L->end = L->qd + align_up(E * S * sizeof(float));
   return MOE_OK;
 }
 
@@ -179,6 +181,7 @@ OrthoArgs ortho_args(const moe_ortho_desc_t* d, const OrthoLayout& L, void* ws) 
   char* b = (char*)ws;
   p.part = (double*)(b + L.part);
   p.x0 = b + L.x0; p.x1 = b + L.x1; p.p = b + L.p; p.q = b + L.q;
+  p.pd = (float*)(b + L.pd); p.qd = (float*)(b + L.qd);
   p.E = (int)d->E; p.M = (int)d->M; p.N = (int)d->N; p.S = (int)(d->M < d->N ? d->M : d->N);
   p.steps = d->steps; p.a = d->a; p.b = d->b; p.c = d->c; p.eps = d->eps;
   p.g_f32 = d->dtype == MOE_F32; p.out_f32 = d->out_dtype == MOE_F32;

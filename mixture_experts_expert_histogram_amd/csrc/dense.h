@@ -8,7 +8,7 @@
 // waits, so the loop covers them itself:
 //
 // * Operands come straight into LDS (buffer loads to LDS, 1 KB a load, whole
-//   128-byte lines) through a ring of NS stages of 64 k.
+//   128-byte lines) through rings of NSA and NSB stages of 64 k.
 // * Fragments are read from LDS two slices of 16 k ahead of their products.
 //   A stage is therefore read to its end half a step before its products are
 //   done, and one barrier in the middle of a step stands for both "this stage
@@ -22,6 +22,11 @@
 // of 128 bytes, whose 16-byte chunks are permuted against bank conflicts by
 // permuting what each lane loads.  A k or a row that does not exist is read as
 // zero (k) or as the last one (row, column; those results are not stored).
+//
+// Bound by the card's power in large products: 8192 x 4096 over 16384 takes 757
+// us (1452 TFLOP/s) with the matrix cores 87 % busy at 1.56 GHz, where matrix
+// instructions alone, on random operands, reach 1830 TFLOP/s at 1.89 GHz (2400
+// on zeros).  Instructions of 16 x 16 results drew the same power.
 #pragma once
 #include <type_traits>
 

@@ -66,15 +66,16 @@ inline float tile_time(const TileKind& k, long tiles, long K) {
 }
 
 // The kind of tile that an M x N product over K, `batch` times, is done with
-// soonest, of those whose tiles a launch holds (the host checks the largest kind).
-inline int tile_kind(long M, long N, long K, long batch = 1) {
-  int best = 0;
+// soonest, of those from `first` on whose tiles a launch holds (the host checks
+// the largest kind).
+inline int tile_kind(long M, long N, long K, long batch = 1, int first = 0) {
+  int best = first;
   float least = 0.f;
-  for (int i = 0; i < N_TILES; ++i) {
+  for (int i = first; i < N_TILES; ++i) {
     const TileKind& k = kTiles[i];
     const long tiles = batch * ((M + 64 * k.fm - 1) / (64 * k.fm)) * ((N + 64 * k.fn - 1) / (64 * k.fn));
     const float t = tile_time(k, tiles, K);
-    if (i == 0 || (t < least && tiles <= MAX_TILES)) best = i, least = t;
+    if (i == first || (t < least && tiles <= MAX_TILES)) best = i, least = t;
   }
   return best;
 }

@@ -11,6 +11,10 @@
 namespace moe {
 namespace dense {
 
+// 8192 tokens, H 4096, I 8192: 666 us (825 TFLOP/s).  The tiles' ends read 1.07
+// GB of gate and up values and write 0.6 GB, all workgroups at about the same
+// time and so without matrix work beside them: some 280 us at 6 TB/s.  Starts
+// put apart by a wait gained 30 us here and lost more in smaller calls.
 // ACT: 0 swiglu, 1 clamped
 template <class C, int ACT>
 __global__ __launch_bounds__(256, 1) void ffn_down_dgrad_kernel(FfnArgs p) {
@@ -89,7 +93,8 @@ __global__ __launch_bounds__(256, 1) void ffn_down_dgrad_kernel(FfnArgs p) {
   }
 }
 
-// dgate[t] = s (1 - s) times the sum of the row's partial sums, in order.
+// dgate[t] = s (1 - s) times the sum of the row's partial sums, in order (7 us for
+// 4096 tokens and 30 sums a row, of which a launch is about 4).
 __global__ __launch_bounds__(256) void ffn_gate_reduce_kernel(FfnArgs p) {
   const int t = blockIdx.x * 256 + threadIdx.x;
   if (t >= p.T) return;
@@ -99,6 +104,7 @@ __global__ __launch_bounds__(256) void ffn_gate_reduce_kernel(FfnArgs p) {
   p.dgate[t] = s * (1.f - s) * v;
 }
 
+// 8192 tokens, H 4096, I 8192: 757 us (1452 TFLOP/s, matrix cores 87 % busy).
 template <class C>
 __global__ __launch_bounds__(256, 1) void ffn_gate_up_dgrad_kernel(FfnArgs p) {
   FFN_PROLOGUE(C)
@@ -124,7 +130,9 @@ __global__ __launch_bounds__(256, 1) void ffn_gate_up_dgrad_kernel(FfnArgs p) {
   }
 }
 
-// dW [M,N] = P^T Q over the T tokens: P [T,M], Q [T,N].
+// dW [M,N] = P^T Q over the T tokens: P [T,M], Q [T,N], both read along their
+// rows with transposing LDS reads.  16384 x 4096 and 4096 x 8192 over 8192 tokens:
+// 774 and 387 us (1421 TFLOP/s, matrix cores 85 and 83 % busy).
 struct WgradArgs {
   const void *P, *Q;
   void* dw;

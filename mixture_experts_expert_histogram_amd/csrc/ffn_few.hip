@@ -7,7 +7,9 @@
 // matrix-core fragments (16 rows x 64 contiguous bytes a load) against 16 token
 // columns, D units in flight a wave.  The partial sums meet in LDS in wave order.
 // Few rows a workgroup and all of its loads in flight at once are what fills
-// the card with one matrix of 2880 x 2880.
+// the card with one matrix of 2880 x 2880 (16 tokens bf16: 24 us for both
+// kernels).  13 tokens fp32, H 1048, I 712: 7.0 and 5.8 us for 9 MB, the two
+// launches' start, first loads and end.
 #include "ffn_tiles.h"
 
 namespace moe {

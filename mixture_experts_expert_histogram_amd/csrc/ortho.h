@@ -4,6 +4,7 @@
 
 namespace moe {
 
+constexpr int ORTHO_EXACT = 64;    // S from which Q's diagonal is corrected by factors (ortho.hip)
 constexpr int ORTHO_PARTS = 256;   // most partial sums of a matrix's squares
 
 // Iterates X and Gram matrices are kept in fp16 with these factors.
@@ -17,6 +18,7 @@ struct OrthoArgs {
   void* out;            // out, or the new weights
   void *x0, *x1;        // fp16 [E,M,N]
   void *p, *q;          // fp16 [E,S,S], S = min(M,N)
+  float *pd, *qd;       // [E,S]: P's diagonal less its fp16 value; Q's, or its quotient by that (S >= ORTHO_EXACT)
   double* part;         // [E][ORTHO_PARTS]
   int E, M, N, S, steps;
   int g_f32, out_f32;

@@ -16,13 +16,24 @@
 // X, P and Q are held in fp16, which the singular values' known range allows
 // (at most 1.21 with the usual coefficients; the host checks others): 11
 // significant bits where bf16 has 8, at the same matrix rate.  With a bf16
-// result the whole is 2.0e-3 from 64 bits in the 2-norm, of which the result's
-// rounding is 1.66e-3; with bf16 iterates it would be 1.1e-2.  a X as a I within
-// Q costs no accuracy (its rounding is one of 11 bits on the diagonal) and
-// leaves the update a plain product, whose epilogue reads nothing.  Factors 2^6 on X
-// and 2^12 on P and Q keep small elements out of the subnormal range.  Sums and
-// the polynomial's terms are fp32, the norm is summed in 64 bits (no overflow
-// or underflow of fp32 gradients' squares).
+// result the whole is 1.8e-3 to 2.1e-3 from 64 bits in the 2-norm, of which the
+// result's rounding is 1.66e-3; with bf16 iterates it would be 1.1e-2.  a X as a
+// I within Q leaves the update a plain product, whose epilogue reads nothing.
+// The diagonals of P and Q hold most of their size, and with it most of their
+// rounding, so what it takes away goes beside them in fp32: P's into Q's
+// diagonal, Q's as a factor of the update's rows (columns of X Q), which scales
+// what lies off the diagonal too, by 1 + 2^-12 at most, or, below ORTHO_EXACT
+// rows, where single elements count, as the missing multiple of X.  Without
+// that 2120 x 104 was 2.5e-3 off, now 1.9e-3, for 0.5 % of the time.
+// Factors 2^6 on X and 2^12 on P and Q keep small elements out of the subnormal
+// range.  Sums and the polynomial's terms are fp32, the norm is summed in 64 bits
+// (no overflow or underflow of fp32 gradients' squares).
+//
+// 16 matrices of 2880 x 2880, five steps: 7.9 ms, a step 404 us for P (66 % of the
+// matrix cores busy at 1.67 GHz), 444 for Q (59 %) and 685 for X (75 %), before
+// them 58 us for the norm and 86 for the first X (4.6 and 6.2 TB/s).  The sides
+// are 11.25 tiles of 256, which count as 12: P and Q compute 23 % more than half
+// a square (their diagonal tiles are whole), X 14 % more than it needs.
 #include "dense_tiles.h"
 #include "ortho.h"
 
@@ -30,6 +41,8 @@ namespace moe {
 namespace dense {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) float lds_float;
+typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
 
@@ -69,7 +82,8 @@ __device__ __forceinline__ double sum_256(double v, double (&red)[4]) {
 }
 
 // The update's squares, summed by workgroup, and a step's new momentum: one
-// pass over g (and m), bound by HBM.
+// pass over g (and m), bound by HBM (a step of 8 matrices of 5760 x 2880 with
+// fp32 gradients: 289 us, 5.5 TB/s).
 template <bool F32>
 __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs p) {
   __shared__ double red[4];
@@ -96,7 +110,8 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs p) {
   if (threadIdx.x == 0) p.part[blockIdx.y * ORTHO_PARTS + blockIdx.x] = sum;
 }
 
-// X = u / (|u| + eps) in fp16, times ORTHO_X; a step's u again from g and m'.
+// X = u / (|u| + eps) in fp16, times ORTHO_X; a step's u again from g and m'
+// (the same step: 260 us, 5.1 TB/s).
 template <bool F32>
 __global__ __launch_bounds__(256) void ortho_scale_kernel(OrthoArgs p, int parts) {
   static_assert(ORTHO_PARTS <= 256, "a partial sum a thread");
@@ -127,13 +142,15 @@ struct SymArgs {
   const uint16_t* a;   // [E] matrices: rows of K (ROWS), or K rows of S
   const uint16_t* p;   // QUAD: [E,S,S], P
   uint16_t* out;       // [E,S,S]
+  const float* pd;     // QUAD: [E,S], P's diagonal less its fp16 value
+  float* diag;         // [E,S]: what the diagonal's rounding takes away, or (QUAD, S >= ORTHO_EXACT) its factor
   size_t a_step;       // elements of a matrix of a
   int E, S, K, tiles;  // tiles: of a side
   float a_diag, b, c;  // QUAD: a_diag I + b P + c A A^T
 };
 
-// out = A A^T (QUAD: a_diag I + b P + c A A^T) for square tiles on and above the diagonal,
-// each stored where it belongs and, mirrored, below.  The mirror goes through
+// out = A A^T (QUAD: a_diag I + b P + c A A^T) for square tiles on and above the
+// diagonal, each stored where it belongs and, mirrored, below.  The mirror goes through
 // LDS: the tile is written there as it lies in the registers and read back with
 // the transposing reads.  COLS: A is held as its transpose (K rows of S).
 template <class C, bool COLS, bool QUAD>
@@ -165,11 +182,17 @@ __global__ __launch_bounds__(256, 1) void ortho_sym_kernel(SymArgs p) {
     mainloop<C, f16x8_t>(as, bs, K, lds, acc, wave, lane);
   }
   const uint16_t* P = p.p + (size_t)S * S * e;
+  float* diag = p.diag + (size_t)S * e;
   uint16_t* out = p.out + (size_t)S * S * e;
   // panels [BM rows][64 columns] of LDS, 16-byte chunks permuted as in FragSrc
   const int r32 = lane & 31, x = (((r32 >> 1) & 1) << 2) | (((r32 >> 3) & 1) << 1);
   struct Held { f16x4_t v[4]; };
   const int c4 = 4 * (lane >> 5);
+  float dr[C::FM] = {};
+  if (QUAD && mt == nt) {
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) dr[i] = p.pd[(size_t)S * e + min(m0 + wm * 32 * C::FM + 32 * i + r32, S - 1)];
+  }
   each_fragment<C, Held, 4>(
       [&](int i, int j, Held& h) __attribute__((always_inline)) {   // rows and columns past the last read the last one
         if (!QUAD) return;
@@ -179,6 +202,8 @@ __global__ __launch_bounds__(256, 1) void ortho_sym_kernel(SymArgs p) {
       },
       [&](int i, int j, const Held& held) __attribute__((always_inline)) {
         const int tr = wm * 32 * C::FM + 32 * i + r32, row = m0 + tr;
+        float mine = 0.f;
+        const bool on_diag = mt == nt && wm * C::FM + i == wn * C::FN + j;   // the diagonal passes through this fragment
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int tc = (wn * C::FN + j) * 32 + 16 * q;
@@ -189,7 +214,15 @@ __global__ __launch_bounds__(256, 1) void ortho_sym_kernel(SymArgs p) {
             for (int k = 0; k < 4; ++k) {
               const float s = acc[i][j][8 * q + 4 * h + k];
               v[h][k] = QUAD ? p.b * (float)held.v[2 * q + h][k] + p.c * s : s;
-              if (QUAD && mt == nt && tr == tc + 8 * h + c4 + k) v[h][k] += p.a_diag;
+            }
+            if (on_diag) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const bool on = r32 == 16 * q + 8 * h + c4 + k;
+                // with P's element as it was before its rounding
+                if (QUAD) v[h][k] += on ? p.a_diag + (p.b + 2.f * p.c * (float)held.v[2 * q + h][k]) * dr[i] : 0.f;
+                mine = on ? v[h][k] : mine;
+              }
             }
             if (mt != nt) {
               const int ct = tc + 8 * h;
@@ -200,6 +233,11 @@ __global__ __launch_bounds__(256, 1) void ortho_sym_kernel(SymArgs p) {
           const u32x4 o = pack_pair_f16(v[0], v[1]);
           const int cc = n0 + tc + 2 * c4;
           if (row < S && cc < S) *(u32x4*)(out + (size_t)row * S + cc) = o;
+        }
+        if (on_diag && (r32 & 4) == c4 && row < S) {   // the lane that holds the row's diagonal element
+          const float r = (float)(_Float16)mine;
+          if (!QUAD || S < ORTHO_EXACT) diag[row] = mine - r;
+          else diag[row] = fabsf(mine) > 0x1p-13f ? mine / r : 1.f;   // a normal number of fp16
         }
       });
   if (mt == nt) return;
@@ -227,6 +265,7 @@ __global__ __launch_bounds__(256, 1) void ortho_sym_kernel(SymArgs p) {
 enum { TO_X = 0, TO_BF16 = 1, TO_F32 = 2 };
 struct UpdateArgs {
   const uint16_t *x, *q;
+  const float* qd;   // [E,S]: for each row (of Q X) or column (of X Q), its factor, or EXACT: the missing multiple of X
   void* out;
   const void* w;   // the weights that a step updates, or null
   int E, M, N, S, mt, nt;
@@ -242,7 +281,7 @@ __device__ __forceinline__ void load4(const float* p, float* v) {
   v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
 }
 
-template <class C, bool WIDE, int TO>
+template <class C, bool WIDE, int TO, bool EXACT>
 __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
   using T = std::conditional_t<TO == TO_F32, float, uint16_t>;
   __shared__ __align__(1024) char lds[C::LDS];
@@ -255,6 +294,7 @@ __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
   const int wm = wave >> 1, wn = wave & 1, m0 = mt * C::BM, n0 = nt * C::BN, M = p.M, N = p.N, S = p.S;
   f32x16 acc[C::FM][C::FN];
   const uint16_t *X = p.x + (size_t)M * N * e, *Q = p.q + (size_t)S * S * e;
+  const float qd = p.qd[(size_t)S * e + min((WIDE ? m0 : n0) + (int)threadIdx.x, S - 1)];   // of tile row or column threadIdx.x
   const auto rows = [&](auto& src, const uint16_t* b, int r0, int n) {   // rows of S
     src.init(b + (size_t)r0 * S, nullptr, [&](int r) { return (uint32_t)(min(r, n - 1 - r0) * S * 2); }, wave, lane);
   };
@@ -274,13 +314,19 @@ __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
   const size_t at = (size_t)M * N * e;
   const int r0 = m0 + wm * 32 * C::FM + (lane & 31), c00 = n0 + wn * 32 * C::FN, c4 = 4 * (lane >> 5);
   const bool step = TO != TO_X && p.w != nullptr;
-  struct Held { float w[4][4]; };
-  each_fragment<C, Held, 2>(
+  lds_float* fac = (lds_float*)lds;
+  if ((int)threadIdx.x < (WIDE ? C::BM : C::BN)) fac[threadIdx.x] = f * qd;
+  __syncthreads();
+  struct Held { float w[4][4]; f16x4_t x[4]; };
+  each_fragment<C, Held, EXACT ? 3 : 2>(
       [&](int i, int j, Held& h) __attribute__((always_inline)) {   // rows and columns past the last read the last one
-        if (!step) return;
         const size_t row = at + (size_t)min(r0 + 32 * i, M - 1) * N;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) load4((const T*)p.w + row + min(c00 + 32 * j + 8 * v, N - 8) + c4, h.w[v]);
+        for (int v = 0; v < 4; ++v) {
+          const size_t el = row + min(c00 + 32 * j + 8 * v, N - 8) + c4;
+          if (step) load4((const T*)p.w + el, h.w[v]);
+          if constexpr (EXACT) h.x[v] = *(const f16x4_t*)(p.x + el);
+        }
       },
       [&](int i, int j, const Held& held) __attribute__((always_inline)) {
         const int row = r0 + 32 * i;
@@ -289,12 +335,17 @@ __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
           const int c = c00 + 32 * j + 16 * q;
           float v[2][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h) {
+            f32x4 d;
+            if constexpr (WIDE) d = f32x4{1.f, 1.f, 1.f, 1.f} * fac[row - m0];
+            else d = *(lds_f32x4*)(fac + (c - n0) + 8 * h + c4);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float o = f * acc[i][j][8 * q + 4 * h + k];
+              const float r = acc[i][j][8 * q + 4 * h + k];
+              const float o = EXACT ? f * r + d[k] * (float)held.x[2 * q + h][k] : d[k] * r;
               v[h][k] = step ? p.keep * held.w[2 * q + h][k] - p.lr * o : o;
             }
+          }
           if constexpr (TO == TO_F32) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -329,12 +380,14 @@ hipError_t sym(SymArgs p, bool cols, bool quad, hipStream_t s) {
 
 template <class C, bool WIDE, int TO>
 hipError_t run_update(const UpdateArgs& p, hipStream_t s) {
-  const auto k = ortho_update_kernel<C, WIDE, TO>;
+  auto k = ortho_update_kernel<C, WIDE, TO, false>;
+  if constexpr (C::FM < 3)
+    if (p.S < ORTHO_EXACT) k = ortho_update_kernel<C, WIDE, TO, true>;
   return run_kernel("ortho_update", s, [&] { k<<<deal_grid((long)p.E * p.mt * p.nt), C::NT, 0, s>>>(p); });
 }
 hipError_t update(UpdateArgs p, int to, hipStream_t s) {
   hipError_t e = hipSuccess;
-  with_tile(tile_kind(p.M, p.N, p.S, p.E), [&](auto c) {
+  with_tile(tile_kind(p.M, p.N, p.S, p.E, p.S < ORTHO_EXACT ? 3 : 0), [&](auto c) {   // 3: tiles of at most 128 rows
     using C = decltype(c);
     p.mt = (p.M + C::BM - 1) / C::BM;
     p.nt = (p.N + C::BN - 1) / C::BN;
@@ -371,10 +424,11 @@ hipError_t launch_ortho(const OrthoArgs& p, hipStream_t s) {
   for (int i = 0; i < p.steps && e == hipSuccess; ++i) {
     const bool last = i + 1 == p.steps;
     // X X^T carries ORTHO_X^2 = ORTHO_P; P P carries ORTHO_P^2
-    e = sym({x, nullptr, P, n, p.E, p.S, wide ? p.N : p.M, 0, 0.f, 0.f, 1.f}, !wide, false, s);
-    if (e == hipSuccess) e = sym({P, P, Q, ss, p.E, p.S, p.S, 0, ORTHO_P * p.a, p.b, p.c / ORTHO_P}, false, true, s);
+    e = sym({x, nullptr, P, nullptr, p.pd, n, p.E, p.S, wide ? p.N : p.M, 0, 0.f, 0.f, 1.f}, !wide, false, s);
     if (e == hipSuccess)
-      e = update({x, Q, last ? p.out : y, last ? p.w : nullptr, p.E, p.M, p.N, p.S, 0, 0, p.lr, p.keep},
+      e = sym({P, P, Q, p.pd, p.qd, ss, p.E, p.S, p.S, 0, ORTHO_P * p.a, p.b, p.c / ORTHO_P}, false, true, s);
+    if (e == hipSuccess)
+      e = update({x, Q, p.qd, last ? p.out : y, last ? p.w : nullptr, p.E, p.M, p.N, p.S, 0, 0, p.lr, p.keep},
                  !last ? TO_X : p.out_f32 ? TO_F32 : TO_BF16, s);
     uint16_t* t = x;
     x = y;

@@ -159,3 +159,31 @@ def test_eps_of_zero(dtype):
     assert torch.count_nonzero(o[2]) == 0
     keep = [0, 1, 3, 4]
     compare(o[keep], u[keep], eps=0.0)
+
+
+def held_off_the_diagonal(u, steps):
+    """The iteration with the kernels' roundings except those of the diagonals of X X^T and Q."""
+    a, b, c = COEF
+
+    def hold(t, scale, keep_diagonal):
+        r = (t * scale).half().double() / scale
+        return r - torch.diag_embed(r.diagonal(dim1=-2, dim2=-1) - t.diagonal(dim1=-2, dim2=-1)) if keep_diagonal else r
+    x = u.double() / u.double().square().sum((-2, -1), keepdim=True).sqrt()
+    x = hold(x.mT.contiguous() if x.shape[-2] > x.shape[-1] else x, 64.0, False)
+    for i in range(steps):
+        p = hold(x @ x.mT.contiguous(), 4096.0, True)
+        x = hold(a * torch.eye(p.shape[-1], dtype=p.dtype, device=p.device) + b * p + c * (p @ p), 4096.0, True) @ x
+        if i + 1 < steps:
+            x = hold(x, 64.0, False)
+    return x.mT.contiguous() if u.shape[-2] > u.shape[-1] else x
+
+
+# Long matrices, whose singular values lie close together and pass where the iteration is steep (|f'| up to 4 at 1.2), so
+# that roundings of the diagonals of X X^T and Q would be most of the error: within twice what the others bring.
+@pytest.mark.parametrize("M,N", [(2120, 104), (96, 5760), (104, 2120), (96, 1000), (600, 64)])
+def test_diagonals_are_not_rounded(M, N):
+    u = updates(2, M, N, seed=M)
+    exact = newton_schulz(u, COEF, 5, 0.0)
+    off = (held_off_the_diagonal(u, 5) - exact).norm().item()
+    o, _ = moe.orthogonalize(u, dtype="fp32", eps=0.0)
+    assert (o.double() - exact).norm().item() <= 2 * off + 2.0 ** -20 * exact.norm().item()
