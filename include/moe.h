@@ -338,7 +338,7 @@ moe_status_t moe_mx_fwd_logits(const moe_desc_t* desc, const void* hidden,
  *     tiles of 256 x 256 in [T, max(2I, H)], else MOE_ERR_UNSUPPORTED.
  *   - a = phi(..) is rounded to the activations' type as the second product's
  *     operand; sums are fp32; out is rounded once.
- *   - Up to 16 tokens (bf16) or 64 (fp32) without `saved` run on kernels that
+ *   - Up to 16 tokens (bf16) or 512 (fp32) without `saved` run on kernels that
  *     read the weights once and make no tiles; their order of sums is their
  *     own.
  *   - `saved` (nullable) receives the gate and up values (fp32, in an order of
@@ -348,7 +348,7 @@ moe_status_t moe_mx_fwd_logits(const moe_desc_t* desc, const void* hidden,
  * s (1 - s) <d_out, y>), d_w_gate_up [2I,H], d_w_down [H,I] in grad_dtype
  * (fp32 sums over the tokens); the gradient of add is d_out.  `saved`: what
  * moe_ffn_fwd left for the same inputs, or NULL (recomputed).  T = 0 writes
- * zero weight gradients.  In fp32 the products of more than 64 tokens, and
+ * zero weight gradients.  In fp32 the products of more than 512 tokens, and
  * the backward pass, are those of moe_fwd / moe_bwd with one expert.
  * Any output of moe_ffn_workspace_size may be NULL. */
 moe_status_t moe_ffn_workspace_size(const moe_desc_t* desc, size_t* fwd_ws,

@@ -8,8 +8,11 @@ namespace moe {
 // Most tokens that the kernels for a few tokens take (weights read once, no
 // tiles); more go to the dense products, in fp32 to those of one expert.  2880
 // x 2880 bf16, both kernels in us: 16 tokens 24 against 26 on tiles of 64 x 64,
-// 17 tokens 30 against 27, 64 tokens 51 against 33.
-constexpr int FFN_FEW_BF16 = 16, FFN_FEW_F32 = 64;
+// 17 tokens 30 against 27, 64 tokens 51 against 33.  fp32, against the products of
+// one expert: 2544 x 3712 64 tokens 100 against 526, 512 tokens 460 against 540,
+// 1024 tokens 891 against 705; 2880 x 2880 494 against 490 and 936 against 660;
+// 1048 x 712 59 against 175 and 97 against 179.
+constexpr int FFN_FEW_BF16 = 16, FFN_FEW_F32 = 512;
 
 struct FfnArgs {
   const void* x;        // [T,H]

@@ -1,6 +1,5 @@
-// The gated feed-forward block for up to 16 tokens (bf16) or 64 (fp32): the time is
-// that of reading 3 H I weights once, and for one token that of two launches and
-// their first loads.
+// The gated feed-forward block for few tokens: the time is that of reading 3 H I
+// weights once, and for one token that of two launches and their first loads.
 //
 // A workgroup takes 16 weight rows (8 gate and 8 up rows, or 16 rows of Wd);
 // its 8 waves split k in units of one 128-byte line a row, read straight into
@@ -9,7 +8,10 @@
 // Few rows a workgroup and all of its loads in flight at once are what fills
 // the card with one matrix of 2880 x 2880 (16 tokens bf16: 24 us for both
 // kernels).  13 tokens fp32, H 1048, I 712: 7.0 and 5.8 us for 9 MB, the two
-// launches' start, first loads and end.
+// launches' start, first loads and end.  In fp32 up to four groups of 16 tokens
+// share a workgroup's weights, and more tokens are more workgroups: 64 tokens of
+// 2544 x 3712 56 and 44 us, 256 tokens 164 and 110 (53 TFLOP/s of the fp32 matrix
+// rate's 157), bound by the token rows that every 16 weight rows read from L2.
 #include "ffn_tiles.h"
 
 namespace moe {
@@ -96,19 +98,32 @@ __device__ __forceinline__ float few_sum(const float* red, int t, int row) {
   return v;
 }
 
+// A workgroup's rows and tokens: its block of rows, and in t0 and nt its group of
+// NT x 16 tokens.  The groups of a block of rows follow one another on one XCD
+// (workgroup w runs on XCD w % 8), which reads the weights once.
+template <int NT>
+__device__ __forceinline__ int few_place(int T, int& t0, int& nt) {
+  const int groups = (T + NT * 16 - 1) / (NT * 16), w = blockIdx.x >> 3, block = w / groups;
+  t0 = (w - block * groups) * NT * 16;
+  nt = min(T - t0, NT * 16);
+  return block * 8 + (blockIdx.x & 7);
+}
+
 template <bool F32, int NT>
 __global__ __launch_bounds__(FEW_NW * 64) void ffn_few_gate_up_kernel(FfnArgs p) {
   using T = std::conditional_t<F32, float, uint16_t>;
   __shared__ __align__(16) float red[FEW_NW * NT * 256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int j0 = blockIdx.x * 8;
+  int t0, nt;
+  const int j0 = few_place<NT>(p.T, t0, nt) * 8;
+  if (j0 >= p.I) return;
   const long row = p.gu_rs * sizeof(T);
   // I is a multiple of 8: the workgroup's 8 columns exist
   const uint32_t wrow = (uint32_t)((lane & 7) * row) + (lane & 8 ? (uint32_t)((const char*)p.gu_u - (const char*)p.gu_g) : 0u);
-  few_dot<F32, NT>(rsrc((const char*)p.gu_g + row * j0), wrow, rsrc(p.x), p.T, p.H, red, wave, lane);
-  for (int o = threadIdx.x; o < 8 * p.T; o += FEW_NW * 64) {
+  few_dot<F32, NT>(rsrc((const char*)p.gu_g + row * j0), wrow, rsrc((const T*)p.x + (size_t)t0 * p.H), nt, p.H, red, wave, lane);
+  for (int o = threadIdx.x; o < 8 * nt; o += FEW_NW * 64) {
     const int j = o & 7, t = o >> 3;
-    store_val<T>((T*)p.a + (size_t)t * p.I + j0 + j,
+    store_val<T>((T*)p.a + (size_t)(t0 + t) * p.I + j0 + j,
                  glu_fwd(few_sum<NT>(red, t, j), few_sum<NT>(red, t, 8 + j), p.act, p.limit, p.alpha));
   }
 }
@@ -121,16 +136,18 @@ __global__ __launch_bounds__(FEW_NW * 64) void ffn_few_down_kernel(FfnArgs p) {
   using T = std::conditional_t<F32, float, uint16_t>;
   __shared__ __align__(16) float red[FEW_NW * NT * 256];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h0 = blockIdx.x * 16;
+  int t0, nt;
+  const int h0 = few_place<NT>(p.T, t0, nt) * 16;
+  if (h0 >= p.H) return;
   const uint32_t row = p.I * sizeof(T);
-  few_dot<F32, NT>(rsrc((const char*)p.wd + (size_t)row * h0), row * min(lane & 15, p.H - 1 - h0), rsrc(p.a), p.T, p.I, red,
-                   wave, lane);
-  for (int o = threadIdx.x; o < 16 * p.T; o += FEW_NW * 64) {
+  few_dot<F32, NT>(rsrc((const char*)p.wd + (size_t)row * h0), row * min(lane & 15, p.H - 1 - h0),
+                   rsrc((const T*)p.a + (size_t)t0 * p.I), nt, p.I, red, wave, lane);
+  for (int o = threadIdx.x; o < 16 * nt; o += FEW_NW * 64) {
     const int h = o & 15, t = o >> 4;
     if (h0 + h >= p.H) continue;
-    const size_t at = (size_t)t * p.H + h0 + h;
+    const size_t at = (size_t)(t0 + t) * p.H + h0 + h;
     const float ad = p.add ? as_float(((const T*)p.add)[at]) : 0.f;
-    store_val<T>((T*)p.out + at, ad + row_gate(p.gate, t) * few_sum<NT>(red, t, h));
+    store_val<T>((T*)p.out + at, ad + row_gate(p.gate, t0 + t) * few_sum<NT>(red, t, h));
   }
 }
 
@@ -232,11 +249,30 @@ hipError_t run_one(const FfnArgs& p, hipStream_t s) {
   return run_kernel("ffn_one_down", s, [&] { ffn_one_down_kernel<F32, N><<<p.H / 4, 256, 0, s>>>(p); });
 }
 
-template <bool F32, int NT>
-hipError_t run_few(const FfnArgs& p, hipStream_t s) {
-  const hipError_t e = run_kernel("ffn_few_gate_up", s, [&] { ffn_few_gate_up_kernel<F32, NT><<<p.I / 8, FEW_NW * 64, 0, s>>>(p); });
-  if (e != hipSuccess) return e;
-  return run_kernel("ffn_few_down", s, [&] { ffn_few_down_kernel<F32, NT><<<(p.H + 15) / 16, FEW_NW * 64, 0, s>>>(p); });
+// Groups of 16 tokens of a workgroup, for that many blocks of rows (bf16: the one
+// group): the fewest rounds of the card, times what a workgroup of them takes.
+// fp32 down products, us with 1, 2 and 4: 32 blocks of k 8192, 64 tokens 35, 47
+// and 75, 256 tokens 66, 49 and 77; 159 of k 3712, 64 tokens 50, 51 and 44.
+template <bool F32>
+int few_groups(int T, int blocks) {
+  constexpr float time[] = {1.f, 1.36f, 2.15f};
+  int best = 0;
+  float least = 0.f;
+  for (int i = 0; F32 && i < 3; ++i) {
+    const float t = (float)((blocks * ((T + (16 << i) - 1) / (16 << i)) + 255) / 256) * time[i];
+    if (i == 0 || t < least) best = i, least = t;
+  }
+  return 1 << best;
+}
+template <bool F32, class Run>
+hipError_t with_groups(int T, int blocks, Run run) {
+  const int n = few_groups<F32>(T, blocks);
+  const int grid = (blocks + 7) / 8 * 8 * ((T + 16 * n - 1) / (16 * n));
+  if constexpr (F32) {
+    if (n == 4) return run(std::integral_constant<int, 4>{}, grid);
+    if (n == 2) return run(std::integral_constant<int, 2>{}, grid);
+  }
+  return run(std::integral_constant<int, 1>{}, grid);
 }
 
 template <bool F32>
@@ -244,11 +280,15 @@ hipError_t few(const FfnArgs& p, hipStream_t s) {
   if (p.T == 1) return run_one<F32, 1>(p, s);
   if (p.T == 2) return run_one<F32, 2>(p, s);
   if (p.T <= 4) return run_one<F32, 4>(p, s);
-  if constexpr (F32) {
-    if (p.T > 32) return run_few<F32, 4>(p, s);
-    if (p.T > 16) return run_few<F32, 2>(p, s);
-  }
-  return run_few<F32, 1>(p, s);
+  const hipError_t e = with_groups<F32>(p.T, p.I / 8, [&](auto n, int grid) {
+    const auto k = ffn_few_gate_up_kernel<F32, decltype(n)::value>;
+    return run_kernel("ffn_few_gate_up", s, [&] { k<<<grid, FEW_NW * 64, 0, s>>>(p); });
+  });
+  if (e != hipSuccess) return e;
+  return with_groups<F32>(p.T, (p.H + 15) / 16, [&](auto n, int grid) {
+    const auto k = ffn_few_down_kernel<F32, decltype(n)::value>;
+    return run_kernel("ffn_few_down", s, [&] { k<<<grid, FEW_NW * 64, 0, s>>>(p); });
+  });
 }
 
 // ------------------------------------------------------------------ the block as one expert (fp32, many tokens)

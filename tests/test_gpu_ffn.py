@@ -215,3 +215,9 @@ def test_gradients_against_differences():
         want = (grad.double() * v.double()).sum().item()
         # h^2 / 6 of a third derivative of order one, and fp32 sums over 2 h
         assert abs(diff - want) <= 2e-3 * abs(want), name
+
+
+@pytest.mark.parametrize("T,H,I", [(511, 136, 72), (512, 72, 136), (513, 136, 72), (100, 1048, 24), (190, 24, 1048), (1100, 264, 200)])
+def test_fp32_groups_of_tokens(T, H, I):
+    """Around the most tokens of the 16-row workgroups, and blocks of rows that do not fill a round of them."""
+    run(inputs(T, H, I, "fp32", seed=T), "swiglu", "interleaved")
