@@ -7,6 +7,7 @@ namespace moe {
 constexpr int NORM_MAX_H = 16384;   // a row in the registers of 1024 threads
 constexpr int NORM_GRID = 512;      // most workgroups of a backward pass (partial sums of the weights' gradients)
 
+constexpr int NORM_SHORT = 256;     // threads of a backward workgroup of several rows
 constexpr int NORM_ROWS = 1 << 21;  // most workgroups (rows) of a forward pass along x
 constexpr int64_t NORM_MAX_T = int64_t(1) << 30;
 

@@ -20,7 +20,9 @@
 // statistics need are read anyway.  The step after a block, bf16, 32768 rows of
 // 4096: forward 185 us (5.8 TB/s), backward 291 us (5.6 TB/s), reduction 5; the
 // norm before one, 4096 rows of 2880: 8.8, 18.7 and 4.0 us.  Workgroups that stay
-// were slower forward (198 to 209 us), two rows ahead no faster backward.
+// were slower forward (198 to 209 us), two rows ahead no faster backward.  Short
+// rows share backward workgroups (32768 rows of 512, column gate, 137 -> 61 us, of
+// 1048 176 -> 119).
 #include "gemm_common.h"
 #include "norm.h"
 
@@ -69,19 +71,20 @@ template <> struct Raw<float> {
 __device__ __forceinline__ float one_value(const uint16_t* p) { return __builtin_bit_cast(float, (uint32_t)*p << 16); }
 __device__ __forceinline__ float one_value(const float* p) { return *p; }
 
-// Sums of N values over the workgroup, in every thread; wave sums meet in
+// Sums of N values over the threads of a row (blockDim.x, whole waves; MANY: a
+// workgroup holds blockDim.y rows), in each of them; wave sums meet in
 // red[waves][4].  Alternate calls use different halves of red, so one barrier a
 // call is enough: a half is written again only after the next call's barrier,
 // which every thread reaches after its reads of this one.
-template <int N>
+template <bool MANY = false, int N>
 __device__ __forceinline__ void block_sum(float (&v)[N], float* red, int& half) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = (blockDim.x + 63) >> 6;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
 #pragma unroll
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) v[i] += __shfl_xor(v[i], d);
   if (nw == 1) return;
-  float* r = red + half * 64;
+  float* r = red + half * 64 + (MANY ? threadIdx.y * nw * 4 : 0);
   half ^= 1;
   if (lane == 0) {
 #pragma unroll
@@ -180,10 +183,14 @@ __global__ __launch_bounds__(1024) void norm_fwd_kernel(NormArgs p) {
 
 // ------------------------------------------------------------------ backward
 // kind: the gate's; MAXT: most threads.  With more than 512 the registers do not
-// hold a second row, so the next one is loaded after the present one.
+// hold a second row, so the next one is loaded after the present one.  With
+// NORM_SHORT a workgroup works on blockDim.y rows at a time (all of them reach
+// every barrier) and adds their sums up at its end: short rows would leave the
+// card to 512 workgroups of one or two waves each.  Two waves a SIMD have to fit
+// (launch bounds of 512).
 template <typename T, bool H_IN, int kind, int MAXT>
-__global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs p) {
-  constexpr bool AHEAD = MAXT <= 512;
+__global__ __launch_bounds__(MAXT < 512 ? 512 : MAXT) void norm_bwd_kernel(NormArgs p) {
+  constexpr bool AHEAD = MAXT <= 512, MANY = MAXT == NORM_SHORT;
   __shared__ float red[128];
   int half = 0;
   const int H = p.H;
@@ -207,16 +214,19 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs p) {
     load_row(r.dn, (const T*)p.d_new, row, H);
     if (H_IN) load_row(r.h, (const T*)p.h, row, H);
   };
-  int row = blockIdx.x;
-  if (AHEAD && row < p.T) fetch(row, r);
-  for (; row < p.T; row += gridDim.x) {
+  const int R = MANY ? blockDim.y : 1, group = MANY ? threadIdx.y : 0, stride = gridDim.x * R;
+  const auto row_of = [&](int first) { return MANY ? min(first + group, p.T - 1) : first; };
+  if (AHEAD) fetch(row_of(blockIdx.x * R), r);
+  for (int first = blockIdx.x * R; first < p.T; first += stride) {
+    const bool live = !MANY || first + group < p.T;   // past the last row: the last one again, and nothing comes of it
+    const int row = row_of(first);
     if (AHEAD) c = r;
     else fetch(row, c);
     float f = p.scale;
     if (kind == GATE_ROW) f *= one_value((const T*)p.gate + row);
     Raw<T> gf[V];
     if (kind == GATE_FULL) load_row(gf, (const T*)p.gate, row, H);
-    if (AHEAD && row + (int)gridDim.x < p.T) fetch(row + gridDim.x, r);
+    if (AHEAD && first + stride < p.T) fetch(row_of(first + stride), r);
     float s[3] = {0.f, 0.f, 0.f};   // x'^2, w_next d_y x', h^2
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -230,7 +240,7 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs p) {
         if (H_IN) s[2] += h[e] * h[e];
       }
     }
-    block_sum(s, red, half);
+    block_sum<MANY>(s, red, half);
     const float rx = rsqrtf(s[0] / H + p.eps), mx = s[1] / H * rx * rx * rx;
     const float rh = post ? rsqrtf(s[2] / H + p.eps) : 1.f;
     float t[V][8];
@@ -245,7 +255,7 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (next) {
-          an[j][e] += dy[e] * x[e] * rx;
+          if (live) an[j][e] += dy[e] * x[e] * rx;
           t[j][e] += rx * w[e] * dy[e] - mx * x[e];
         }
         if (H_IN) {
@@ -253,18 +263,18 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs p) {
           const float d = f * (kind >= GATE_COLUMN ? g[e] : 1.f) * t[j][e];
           if (post) {
             q[0] += u[e] * d * h[e];
-            ap[j][e] += d * h[e] * rh;
+            if (live) ap[j][e] += d * h[e] * rh;
           }
           q[1] += t[j][e] * n;
-          if (kind == GATE_COLUMN) ag[j][e] += p.scale * t[j][e] * n;
+          if (kind == GATE_COLUMN && live) ag[j][e] += p.scale * t[j][e] * n;
         }
       }
       const int col = column(j);
-      if (col < H) Raw<T>::store((T*)p.d_x + (size_t)row * H + col, t[j]);
+      if (live && col < H) Raw<T>::store((T*)p.d_x + (size_t)row * H + col, t[j]);
     }
     if (!H_IN) continue;
-    if (post || kind == GATE_ROW) block_sum(q, red, half);
-    if (kind == GATE_ROW && threadIdx.x == 0) ((float*)p.d_gate)[row] = p.scale * q[1];
+    if (post || kind == GATE_ROW) block_sum<MANY>(q, red, half);
+    if (kind == GATE_ROW && live && threadIdx.x == 0) ((float*)p.d_gate)[row] = p.scale * q[1];
     const float mh = q[0] / H * rh * rh * rh;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -279,11 +289,33 @@ __global__ __launch_bounds__(MAXT) void norm_bwd_kernel(NormArgs p) {
         dg[e] = p.scale * t[j][e] * (post ? h[e] * rh * u[e] : h[e]);
       }
       const int col = column(j);
-      if (col < H) {
+      if (live && col < H) {
         Raw<T>::store((T*)p.d_h + (size_t)row * H + col, dh);
         if (kind == GATE_FULL) Raw<T>::store((T*)p.d_gate + (size_t)row * H + col, dg);
       }
     }
+  }
+  if constexpr (MANY) {   // at most NORM_SHORT threads, 16 columns each
+    __shared__ float sums[16 * NORM_SHORT];
+    const auto join = [&](float (&a)[V][8]) {
+      __syncthreads();
+      float* own = sums + (group * blockDim.x + threadIdx.x) * 16;   // read only by the same column's threads
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) own[(j * 8 + e) ^ (threadIdx.x & 15)] = a[j][e];
+      __syncthreads();
+      if (group > 0) return;
+      for (int g = 1; g < R; ++g)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) a[j][e] += own[g * blockDim.x * 16 + ((j * 8 + e) ^ (threadIdx.x & 15))];
+    };
+    if (next) join(an);
+    if (post) join(ap);
+    if (kind == GATE_COLUMN) join(ag);
+    if (group > 0) return;
   }
   float* part = p.part + (size_t)blockIdx.x * 3 * H;
 #pragma unroll
@@ -346,7 +378,7 @@ hipError_t fwd(const NormArgs& p, hipStream_t s) {
 }
 
 template <typename T, int MAXT>
-void run_bwd(const NormArgs& p, int grid, int nt, hipStream_t s) {
+void run_bwd(const NormArgs& p, int grid, dim3 nt, hipStream_t s) {
   if (!p.h) norm_bwd_kernel<T, false, GATE_NONE, MAXT><<<grid, nt, 0, s>>>(p);
   else if (p.gate_kind == GATE_NONE) norm_bwd_kernel<T, true, GATE_NONE, MAXT><<<grid, nt, 0, s>>>(p);
   else if (p.gate_kind == GATE_ROW) norm_bwd_kernel<T, true, GATE_ROW, MAXT><<<grid, nt, 0, s>>>(p);
@@ -356,10 +388,13 @@ void run_bwd(const NormArgs& p, int grid, int nt, hipStream_t s) {
 
 template <typename T>
 hipError_t bwd(const NormArgs& p, hipStream_t s) {
-  const int nt = norm_threads(p.H), grid = p.T < NORM_GRID ? p.T : NORM_GRID;
+  // rows of a workgroup: as many as fit NORM_SHORT threads and leave every workgroup some
+  const int nt = norm_threads(p.H), fit = nt < NORM_SHORT ? NORM_SHORT / nt : 1, want = (int)(((long)p.T + NORM_GRID - 1) / NORM_GRID);
+  const int R = want < 1 ? 1 : fit < want ? fit : want, all = (p.T + R - 1) / R, grid = all < NORM_GRID ? all : NORM_GRID;
   if (grid > 0) {
     const hipError_t e = run_kernel("norm_bwd", s, [&] {
-      if (nt <= 512) run_bwd<T, 512>(p, grid, nt, s);
+      if (R > 1) run_bwd<T, NORM_SHORT>(p, grid, dim3(nt, R), s);
+      else if (nt <= 512) run_bwd<T, 512>(p, grid, nt, s);
       else run_bwd<T, 1024>(p, grid, nt, s);
     });
     if (e != hipSuccess) return e;

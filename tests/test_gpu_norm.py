@@ -211,3 +211,11 @@ def test_more_rows_than_one_dimension_of_a_launch():
     for t0 in range(0, T, 1 << 24):
         n = Norm(x[t0:t0 + (1 << 24)], w, 1e-5)
         check(y[t0:t0 + (1 << 24)], n.n, SECOND * (n.en + half_step(torch.bfloat16) * n.n.abs()), "y")
+
+
+@pytest.mark.parametrize("gate", ["none", "row", "column", "full"])
+@pytest.mark.parametrize("T,H", [(513, 1032), (1025, 2048), (700, 512), (1537, 1024), (2051, 8), (1300, 2056)])
+def test_short_rows_share_workgroups(T, H, gate):
+    """Rows that do not fill the last workgroup of several, at one and two waves a row and past them."""
+    for dtype in TYPES:
+        residual_case(inputs(T, H, dtype, gate, seed=T + H), gate)
