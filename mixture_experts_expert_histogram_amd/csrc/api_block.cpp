@@ -126,7 +126,7 @@ NormArgs norm_args(const moe_norm_desc_t* d) {
 
 // ------------------------------------------------------------ orthogonalisation
 struct OrthoLayout {
-  size_t part, x0, x1, p, q, pd, qd, end;
+  size_t part, x0, x1, l0, l1, p, q, pd, qd, end;
 };
 
 // Largest sizes of the iterates' singular values s, and of b x + c x^2 and a + b
@@ -167,8 +167,11 @@ moe_status_t ortho_check(const moe_ortho_desc_t* d, OrthoLayout* L) {
   const size_t S = (size_t)(d->M < d->N ? d->M : d->N), E = (size_t)d->E;
   L->part = 0;
   L->x0 = align_up(E * ORTHO_PARTS * sizeof(double));
-  L->x1 = L->x0 + align_up(E * d->M * d->N * 2);
-  L->p = L->x1 + align_up(E * d->M * d->N * 2);
+  const size_t x = align_up(E * d->M * d->N * 2);
+  L->x1 = L->x0 + x;
+  L->l0 = L->x1 + x;
+  L->l1 = L->l0 + x;
+  L->p = L->l1 + x;
   L->q = L->p + align_up(E * S * S * 2);
   L->pd = L->q + align_up(E * S * S * 2);
   L->qd = L->pd + align_up(E * S * sizeof(float));
@@ -180,7 +183,7 @@ OrthoArgs ortho_args(const moe_ortho_desc_t* d, const OrthoLayout& L, void* ws) 
   OrthoArgs p = {};
   char* b = (char*)ws;
   p.part = (double*)(b + L.part);
-  p.x0 = b + L.x0; p.x1 = b + L.x1; p.p = b + L.p; p.q = b + L.q;
+  p.x0 = b + L.x0; p.x1 = b + L.x1; p.l0 = b + L.l0; p.l1 = b + L.l1; p.p = b + L.p; p.q = b + L.q;
   p.pd = (float*)(b + L.pd); p.qd = (float*)(b + L.qd);
   p.E = (int)d->E; p.M = (int)d->M; p.N = (int)d->N; p.S = (int)(d->M < d->N ? d->M : d->N);
   p.steps = d->steps; p.a = d->a; p.b = d->b; p.c = d->c; p.eps = d->eps;

@@ -4,11 +4,12 @@
 
 namespace moe {
 
-constexpr int ORTHO_EXACT = 64;    // S from which Q's diagonal is corrected by factors (ortho.hip)
+constexpr int ORTHO_NARROW = 64;   // S below which the update's tiles have at most 128 rows and columns
 constexpr int ORTHO_PARTS = 256;   // most partial sums of a matrix's squares
 
-// Iterates X and Gram matrices are kept in fp16 with these factors.
-constexpr float ORTHO_X = 64.f, ORTHO_P = 4096.f;
+// Iterates X and Gram matrices are kept in fp16 with these factors, what X's
+// rounding leaves in fp16 with ORTHO_LOW more.
+constexpr float ORTHO_X = 64.f, ORTHO_P = 4096.f, ORTHO_LOW = 2048.f;
 
 struct OrthoArgs {
   const void* g;        // [E,M,N] gradients
@@ -17,8 +18,9 @@ struct OrthoArgs {
   const void* w;        // [E,M,N] weights, or null: out receives the orthogonalised update
   void* out;            // out, or the new weights
   void *x0, *x1;        // fp16 [E,M,N]
+  void *l0, *l1;        // fp16 [E,M,N]: what is left of X beside them
   void *p, *q;          // fp16 [E,S,S], S = min(M,N)
-  float *pd, *qd;       // [E,S]: P's diagonal less its fp16 value; Q's, or its quotient by that (S >= ORTHO_EXACT)
+  float *pd, *qd;       // [E,S]: what the fp16 diagonals of P and Q leave out
   double* part;         // [E][ORTHO_PARTS]
   int E, M, N, S, steps;
   int g_f32, out_f32;

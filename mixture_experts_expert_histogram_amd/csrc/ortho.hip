@@ -13,27 +13,37 @@
 // the larger side).  No operand is ever transposed in memory: the products
 // that contract over rows read their operands with transposing LDS reads.
 //
-// X, P and Q are held in fp16, which the singular values' known range allows
-// (at most 1.21 with the usual coefficients; the host checks others): 11
-// significant bits where bf16 has 8, at the same matrix rate.  With a bf16
-// result the whole is 1.8e-3 to 2.1e-3 from 64 bits in the 2-norm, of which the
-// result's rounding is 1.66e-3; with bf16 iterates it would be 1.1e-2.  a X as a
-// I within Q leaves the update a plain product, whose epilogue reads nothing.
-// The diagonals of P and Q hold most of their size, and with it most of their
-// rounding, so what it takes away goes beside them in fp32: P's into Q's
-// diagonal, Q's as a factor of the update's rows (columns of X Q), which scales
-// what lies off the diagonal too, by 1 + 2^-12 at most, or, below ORTHO_EXACT
-// rows, where single elements count, as the missing multiple of X.  Without
-// that 2120 x 104 was 2.5e-3 off, now 1.9e-3, for 0.5 % of the time.
+// P, Q and the products' X are fp16, which the singular values' known range
+// allows (at most 1.21 with the usual coefficients; the host checks others): 11
+// significant bits where bf16 has 8, at the same matrix rate.  X itself is a pair
+// of fp16 values, 22 bits: the rounding of a matrix of low rank (the gradient of an
+// expert with few slots) lies outside of its range for the most part, where each
+// step multiplies it by a.  With one value a 512 x 512 matrix of rank 1 was 0.15
+// off, of rank 64 0.021; now 2.4e-4 and 7.6e-4.  The low half takes part in no
+// product:
+//
+//   X <- Q X = D X + (Q - D) X_high,   D a diagonal
+//
+// costs reads and writes, not matrix work.  What X_high's rounding, r, does is (Q -
+// D) r: nothing outside of X's range with D = a I, and least within it with D =
+// diag(Q).  What is left outside grows by a with every later step, so D is a I,
+// and diag(Q) in the last two steps.  D is kept in fp32 and takes up what the
+// rounding of the rest of Q's diagonal leaves out; what P's diagonal's rounding
+// takes away goes into Q's.  From the iteration in 64 bits, in the 2-norm: 1.5e-3
+// at most from 64 x 64 on, at any rank, 5e-4 to 8e-4 mostly; up to 4e-3 in matrices
+// of 8 rows, where a few roundings are all of it; a bf16 result's own rounding,
+// 1.66e-3, comes on top.  (With all of Q's products on the pair: 1e-4 to 1.1e-3,
+// for another 2 S^2 L operations a step.)
 // Factors 2^6 on X and 2^12 on P and Q keep small elements out of the subnormal
 // range.  Sums and the polynomial's terms are fp32, the norm is summed in 64 bits
 // (no overflow or underflow of fp32 gradients' squares).
 //
-// 16 matrices of 2880 x 2880, five steps: 7.9 ms, a step 404 us for P (66 % of the
-// matrix cores busy at 1.67 GHz), 444 for Q (59 %) and 685 for X (75 %), before
-// them 58 us for the norm and 86 for the first X (4.6 and 6.2 TB/s).  The sides
-// are 11.25 tiles of 256, which count as 12: P and Q compute 23 % more than half
-// a square (their diagonal tiles are whole), X 14 % more than it needs.
+// 16 matrices of 2880 x 2880, five steps: 8.85 ms, a step 415 us for P, 457 for Q
+// and 872 for X (712 without the pair, whose reads and writes at the tiles' ends
+// have no matrix work beside them), before them 53 us for the norm and 130 for the
+// first X.  The sides are 11.25 tiles of 256, which count as 12, and diagonal tiles
+// are whole: P and Q compute 23 % more than half a square, X 14 % more than it
+// needs.
 #include "dense_tiles.h"
 #include "ortho.h"
 
@@ -58,6 +68,18 @@ __device__ __forceinline__ u32x4 pack_pair_f16(const float* lo, const float* hi)
 }
 
 // ------------------------------------------------------------------ norm and first iterate
+// x (times ORTHO_X) as its fp16 value, and what that leaves.
+__device__ __forceinline__ float low_half(float x) { return (x - (float)(_Float16)x) * ORTHO_LOW; }
+// The two groups of four that pack_pair_f16 joined.
+__device__ __forceinline__ void unpack_pair_f16(u32x4 w, float* lo, float* hi) {
+  const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+  const f16x2_t l0 = __builtin_bit_cast(f16x2_t, (uint32_t)a[0]), l1 = __builtin_bit_cast(f16x2_t, (uint32_t)b[0]);
+  const f16x2_t h0 = __builtin_bit_cast(f16x2_t, (uint32_t)a[1]), h1 = __builtin_bit_cast(f16x2_t, (uint32_t)b[1]);
+  lo[0] = (float)l0[0]; lo[1] = (float)l0[1]; lo[2] = (float)l1[0]; lo[3] = (float)l1[1];
+  hi[0] = (float)h0[0]; hi[1] = (float)h0[1]; hi[2] = (float)h1[0]; hi[3] = (float)h1[1];
+}
+
 // 8 gradients (or updates) from element i on.
 template <bool F32>
 __device__ __forceinline__ void load8(const void* p, size_t i, float* v) {
@@ -110,7 +132,7 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs p) {
   if (threadIdx.x == 0) p.part[blockIdx.y * ORTHO_PARTS + blockIdx.x] = sum;
 }
 
-// X = u / (|u| + eps) in fp16, times ORTHO_X; a step's u again from g and m'
+// X = u / (|u| + eps), times ORTHO_X, in two halves; a step's u again from g and m'
 // (the same step: 260 us, 5.1 TB/s).
 template <bool F32>
 __global__ __launch_bounds__(256) void ortho_scale_kernel(OrthoArgs p, int parts) {
@@ -134,6 +156,10 @@ __global__ __launch_bounds__(256) void ortho_scale_kernel(OrthoArgs p, int parts
     for (int e = 0; e < 8; ++e) u[e] *= f, u[e] *= f2;
     *(uint4*)((uint16_t*)p.x0 + at + i) = make_uint4(pack_f16(u[0], u[1]), pack_f16(u[2], u[3]), pack_f16(u[4], u[5]),
                                                     pack_f16(u[6], u[7]));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = low_half(u[e]);
+    *(uint4*)((uint16_t*)p.l0 + at + i) = make_uint4(pack_f16(u[0], u[1]), pack_f16(u[2], u[3]), pack_f16(u[4], u[5]),
+                                                    pack_f16(u[6], u[7]));
   }
 }
 
@@ -143,13 +169,14 @@ struct SymArgs {
   const uint16_t* p;   // QUAD: [E,S,S], P
   uint16_t* out;       // [E,S,S]
   const float* pd;     // QUAD: [E,S], P's diagonal less its fp16 value
-  float* diag;         // [E,S]: what the diagonal's rounding takes away, or (QUAD, S >= ORTHO_EXACT) its factor
+  float* diag;         // [E,S]: what the stored diagonal leaves out
   size_t a_step;       // elements of a matrix of a
   int E, S, K, tiles;  // tiles: of a side
-  float a_diag, b, c;  // QUAD: a_diag I + b P + c A A^T
+  float a_diag, b, c;  // QUAD: a_diag I + b P + c A A^T, a_diag never stored
+  int keep_diag;       // QUAD: b P + c A A^T has its diagonal stored, else zeros there
 };
 
-// out = A A^T (QUAD: a_diag I + b P + c A A^T) for square tiles on and above the
+// out = A A^T (QUAD: b P + c A A^T) for square tiles on and above the
 // diagonal, each stored where it belongs and, mirrored, below.  The mirror goes through
 // LDS: the tile is written there as it lies in the registers and read back with
 // the transposing reads.  COLS: A is held as its transpose (K rows of S).
@@ -220,8 +247,9 @@ __global__ __launch_bounds__(256, 1) void ortho_sym_kernel(SymArgs p) {
               for (int k = 0; k < 4; ++k) {
                 const bool on = r32 == 16 * q + 8 * h + c4 + k;
                 // with P's element as it was before its rounding
-                if (QUAD) v[h][k] += on ? p.a_diag + (p.b + 2.f * p.c * (float)held.v[2 * q + h][k]) * dr[i] : 0.f;
+                if (QUAD) v[h][k] += on ? (p.b + 2.f * p.c * (float)held.v[2 * q + h][k]) * dr[i] : 0.f;
                 mine = on ? v[h][k] : mine;
+                if (QUAD && on && !p.keep_diag) v[h][k] = 0.f;
               }
             }
             if (mt != nt) {
@@ -235,9 +263,8 @@ __global__ __launch_bounds__(256, 1) void ortho_sym_kernel(SymArgs p) {
           if (row < S && cc < S) *(u32x4*)(out + (size_t)row * S + cc) = o;
         }
         if (on_diag && (r32 & 4) == c4 && row < S) {   // the lane that holds the row's diagonal element
-          const float r = (float)(_Float16)mine;
-          if (!QUAD || S < ORTHO_EXACT) diag[row] = mine - r;
-          else diag[row] = fabsf(mine) > 0x1p-13f ? mine / r : 1.f;   // a normal number of fp16
+          const float r = QUAD && !p.keep_diag ? 0.f : (float)(_Float16)mine;
+          diag[row] = QUAD ? p.a_diag + (mine - r) : mine - r;
         }
       });
   if (mt == nt) return;
@@ -264,9 +291,10 @@ __global__ __launch_bounds__(256, 1) void ortho_sym_kernel(SymArgs p) {
 // ------------------------------------------------------------------ X <- Q X (or X Q)
 enum { TO_X = 0, TO_BF16 = 1, TO_F32 = 2 };
 struct UpdateArgs {
-  const uint16_t *x, *q;
-  const float* qd;   // [E,S]: for each row (of Q X) or column (of X Q), its factor, or EXACT: the missing multiple of X
+  const uint16_t *x, *low, *q;
+  const float* qd;   // [E,S]: for each row (of Q X) or column (of X Q) the multiple of X that q's products leave out
   void* out;
+  uint16_t* out_low; // TO_X
   const void* w;   // the weights that a step updates, or null
   int E, M, N, S, mt, nt;
   float lr, keep;
@@ -281,7 +309,7 @@ __device__ __forceinline__ void load4(const float* p, float* v) {
   v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
 }
 
-template <class C, bool WIDE, int TO, bool EXACT>
+template <class C, bool WIDE, int TO>
 __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
   using T = std::conditional_t<TO == TO_F32, float, uint16_t>;
   __shared__ __align__(1024) char lds[C::LDS];
@@ -293,6 +321,9 @@ __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1, m0 = mt * C::BM, n0 = nt * C::BN, M = p.M, N = p.N, S = p.S;
   f32x16 acc[C::FM][C::FN];
+  const size_t at = (size_t)M * N * e;
+  const int r0 = m0 + wm * 32 * C::FM + (lane & 31), c00 = n0 + wn * 32 * C::FN, c4 = 4 * (lane >> 5);
+  const bool step = TO != TO_X && p.w != nullptr;
   const uint16_t *X = p.x + (size_t)M * N * e, *Q = p.q + (size_t)S * S * e;
   const float qd = p.qd[(size_t)S * e + min((WIDE ? m0 : n0) + (int)threadIdx.x, S - 1)];   // of tile row or column threadIdx.x
   const auto rows = [&](auto& src, const uint16_t* b, int r0, int n) {   // rows of S
@@ -311,29 +342,31 @@ __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
     mainloop<C, f16x8_t>(as, bs, S, lds, acc, wave, lane);
   }
   const float f = TO == TO_X ? 1.f / ORTHO_P : 1.f / (ORTHO_X * ORTHO_P);   // the products carry ORTHO_X ORTHO_P
-  const size_t at = (size_t)M * N * e;
-  const int r0 = m0 + wm * 32 * C::FM + (lane & 31), c00 = n0 + wn * 32 * C::FN, c4 = 4 * (lane >> 5);
-  const bool step = TO != TO_X && p.w != nullptr;
   lds_float* fac = (lds_float*)lds;
   if ((int)threadIdx.x < (WIDE ? C::BM : C::BN)) fac[threadIdx.x] = f * qd;
   __syncthreads();
-  struct Held { float w[4][4]; f16x4_t x[4]; };
-  each_fragment<C, Held, EXACT ? 3 : 2>(
+  struct Held { float w[4][4]; u32x4 x[2], low[2]; };
+  each_fragment<C, Held, TO == TO_X ? 4 : 2>(
       [&](int i, int j, Held& h) __attribute__((always_inline)) {   // rows and columns past the last read the last one
         const size_t row = at + (size_t)min(r0 + 32 * i, M - 1) * N;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const size_t el = row + min(c00 + 32 * j + 8 * v, N - 8) + c4;
-          if (step) load4((const T*)p.w + el, h.w[v]);
-          if constexpr (EXACT) h.x[v] = *(const f16x4_t*)(p.x + el);
+        for (int q = 0; q < 2; ++q) {
+          const size_t el = row + min(c00 + 32 * j + 16 * q + 2 * c4, N - 8);
+          h.x[q] = *(const u32x4*)(p.x + el);
+          h.low[q] = *(const u32x4*)(p.low + el);
         }
+        if (!step) return;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) load4((const T*)p.w + row + min(c00 + 32 * j + 8 * v, N - 8) + c4, h.w[v]);
       },
       [&](int i, int j, const Held& held) __attribute__((always_inline)) {
         const int row = r0 + 32 * i;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int c = c00 + 32 * j + 16 * q;
-          float v[2][4];
+          float v[2][4], x[2][4], low[2][4];
+          unpack_pair_f16(held.x[q], x[0], x[1]);
+          unpack_pair_f16(held.low[q], low[0], low[1]);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             f32x4 d;
@@ -342,7 +375,7 @@ __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float r = acc[i][j][8 * q + 4 * h + k];
-              const float o = EXACT ? f * r + d[k] * (float)held.x[2 * q + h][k] : d[k] * r;
+              const float o = f * r + d[k] * (x[h][k] + low[h][k] * (1.f / ORTHO_LOW));
               v[h][k] = step ? p.keep * held.w[2 * q + h][k] - p.lr * o : o;
             }
           }
@@ -354,7 +387,16 @@ __global__ __launch_bounds__(256, 1) void ortho_update_kernel(UpdateArgs p) {
           } else {
             const u32x4 o = TO == TO_X ? pack_pair_f16(v[0], v[1]) : pack_pair(v[0], v[1]);
             const int cc = c + 2 * c4;
-            if (row < M && cc < N) *(u32x4*)((uint16_t*)p.out + at + (size_t)row * N + cc) = o;
+            const size_t el = at + (size_t)row * N + cc;
+            if (row < M && cc < N) *(u32x4*)((uint16_t*)p.out + el) = o;
+            if constexpr (TO == TO_X) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[h][k] = low_half(v[h][k]);
+              const u32x4 l = pack_pair_f16(v[0], v[1]);
+              if (row < M && cc < N) *(u32x4*)(p.out_low + el) = l;
+            }
           }
         }
       });
@@ -380,14 +422,12 @@ hipError_t sym(SymArgs p, bool cols, bool quad, hipStream_t s) {
 
 template <class C, bool WIDE, int TO>
 hipError_t run_update(const UpdateArgs& p, hipStream_t s) {
-  auto k = ortho_update_kernel<C, WIDE, TO, false>;
-  if constexpr (C::FM < 3)
-    if (p.S < ORTHO_EXACT) k = ortho_update_kernel<C, WIDE, TO, true>;
+  const auto k = ortho_update_kernel<C, WIDE, TO>;
   return run_kernel("ortho_update", s, [&] { k<<<deal_grid((long)p.E * p.mt * p.nt), C::NT, 0, s>>>(p); });
 }
 hipError_t update(UpdateArgs p, int to, hipStream_t s) {
   hipError_t e = hipSuccess;
-  with_tile(tile_kind(p.M, p.N, p.S, p.E, p.S < ORTHO_EXACT ? 3 : 0), [&](auto c) {   // 3: tiles of at most 128 rows
+  with_tile(tile_kind(p.M, p.N, p.S, p.E, p.S < ORTHO_NARROW ? 3 : 0), [&](auto c) {   // 3: tiles of at most 128 x 128
     using C = decltype(c);
     p.mt = (p.M + C::BM - 1) / C::BM;
     p.nt = (p.N + C::BN - 1) / C::BN;
@@ -419,20 +459,19 @@ hipError_t launch_ortho(const OrthoArgs& p, hipStream_t s) {
     else ortho_scale_kernel<false><<<dim3(parts, p.E), 256, 0, s>>>(p, parts);
   });
   const bool wide = p.M <= p.N;
-  uint16_t *x = (uint16_t*)p.x0, *y = (uint16_t*)p.x1, *P = (uint16_t*)p.p, *Q = (uint16_t*)p.q;
+  uint16_t *x = (uint16_t*)p.x0, *y = (uint16_t*)p.x1, *xl = (uint16_t*)p.l0, *yl = (uint16_t*)p.l1, *P = (uint16_t*)p.p, *Q = (uint16_t*)p.q;
   const size_t ss = (size_t)p.S * p.S;
   for (int i = 0; i < p.steps && e == hipSuccess; ++i) {
     const bool last = i + 1 == p.steps;
     // X X^T carries ORTHO_X^2 = ORTHO_P; P P carries ORTHO_P^2
-    e = sym({x, nullptr, P, nullptr, p.pd, n, p.E, p.S, wide ? p.N : p.M, 0, 0.f, 0.f, 1.f}, !wide, false, s);
+    e = sym({x, nullptr, P, nullptr, p.pd, n, p.E, p.S, wide ? p.N : p.M, 0, 0.f, 0.f, 1.f, 1}, !wide, false, s);
     if (e == hipSuccess)
-      e = sym({P, P, Q, p.pd, p.qd, ss, p.E, p.S, p.S, 0, ORTHO_P * p.a, p.b, p.c / ORTHO_P}, false, true, s);
+      e = sym({P, P, Q, p.pd, p.qd, ss, p.E, p.S, p.S, 0, ORTHO_P * p.a, p.b, p.c / ORTHO_P, i + 2 < p.steps}, false, true, s);
     if (e == hipSuccess)
-      e = update({x, Q, p.qd, last ? p.out : y, last ? p.w : nullptr, p.E, p.M, p.N, p.S, 0, 0, p.lr, p.keep},
+      e = update({x, xl, Q, p.qd, last ? p.out : y, yl, last ? p.w : nullptr, p.E, p.M, p.N, p.S, 0, 0, p.lr, p.keep},
                  !last ? TO_X : p.out_f32 ? TO_F32 : TO_BF16, s);
-    uint16_t* t = x;
-    x = y;
-    y = t;
+    std::swap(x, y);
+    std::swap(xl, yl);
   }
   return e;
 }
