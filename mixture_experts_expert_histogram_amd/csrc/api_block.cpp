@@ -257,7 +257,7 @@ moe_status_t moe_ffn_bwd(const moe_desc_t* desc, const void* x, const void* w_ga
     TRY(launched(launch_ffn_one_expert(gate, (int)desc->T, ids, w, stream)));
     TRY(moe_bwd(desc, x, ids, w, w_gate_up, w_down, d_out, saved, saved_bytes, d_x, dw, d_w_gate_up, d_w_down,
                 b + L.b_route, ws_bytes - L.b_route, stream));
-    return gate ? launched(launch_ffn_dgate(w, dw, (int)desc->T, d_gate, stream)) : MOE_OK;
+    return gate ? launched(launch_ffn_dgate(gate, dw, (int)desc->T, d_gate, stream)) : MOE_OK;
   }
   FfnArgs p = ffn_args(desc, x, w_gate_up, w_down, gate);
   p.dout = d_out;

@@ -55,7 +55,7 @@ hipError_t launch_ffn_few(int dtype, FfnArgs p, hipStream_t s);  // out, by way 
 // ids[t] = 0 and w[t] = sigmoid(gate[t]) (1 without a gate): the block as a layer of one expert
 hipError_t launch_ffn_one_expert(const float* gate, int T, int32_t* ids, float* w, hipStream_t s);
 hipError_t launch_ffn_add(const float* add, const float* y, long n, float* out, hipStream_t s);   // out = add + y
-// dgate[t] = w (1 - w) dw[t]
-hipError_t launch_ffn_dgate(const float* w, const float* dw, int T, float* dgate, hipStream_t s);
+// dgate[t] = s (1 - s) dw[t], s = sigmoid(gate[t])
+hipError_t launch_ffn_dgate(const float* gate, const float* dw, int T, float* dgate, hipStream_t s);
 
 }  // namespace moe

@@ -100,8 +100,7 @@ __global__ __launch_bounds__(256) void ffn_gate_reduce_kernel(FfnArgs p) {
   if (t >= p.T) return;
   float v = 0.f;
   for (int i = 0; i < p.parts; ++i) v += p.part[(size_t)t * p.parts + i];
-  const float s = row_gate(p.gate, t);
-  p.dgate[t] = s * (1.f - s) * v;
+  p.dgate[t] = gate_slope(p.gate[t]) * v;
 }
 
 // 8192 tokens, H 4096, I 8192: 757 us (1452 TFLOP/s, matrix cores 87 % busy).

@@ -302,9 +302,9 @@ __global__ __launch_bounds__(256) void ffn_add_kernel(const float* add, const fl
   for (long i = blockIdx.x * 256l + threadIdx.x; i < n4; i += gridDim.x * 256l)
     *(f32x4*)(out + 4 * i) = *(const f32x4*)(add + 4 * i) + *(const f32x4*)(y + 4 * i);
 }
-__global__ __launch_bounds__(256) void ffn_dgate_kernel(const float* w, const float* dw, int T, float* dgate) {
+__global__ __launch_bounds__(256) void ffn_dgate_kernel(const float* gate, const float* dw, int T, float* dgate) {
   const int t = blockIdx.x * 256 + threadIdx.x;
-  if (t < T) dgate[t] = w[t] * (1.f - w[t]) * dw[t];
+  if (t < T) dgate[t] = gate_slope(gate[t]) * dw[t];
 }
 
 }  // namespace dense
@@ -320,8 +320,8 @@ hipError_t launch_ffn_add(const float* add, const float* y, long n, float* out, 
   const long g = (n / 4 + 255) / 256;
   return run_kernel("ffn_add", s, [&] { ffn_add_kernel<<<(int)(g < 4096 ? g : 4096), 256, 0, s>>>(add, y, n / 4, out); });
 }
-hipError_t launch_ffn_dgate(const float* w, const float* dw, int T, float* dgate, hipStream_t s) {
-  return run_kernel("ffn_dgate", s, [&] { ffn_dgate_kernel<<<(T + 255) / 256, 256, 0, s>>>(w, dw, T, dgate); });
+hipError_t launch_ffn_dgate(const float* gate, const float* dw, int T, float* dgate, hipStream_t s) {
+  return run_kernel("ffn_dgate", s, [&] { ffn_dgate_kernel<<<(T + 255) / 256, 256, 0, s>>>(gate, dw, T, dgate); });
 }
 
 }  // namespace moe

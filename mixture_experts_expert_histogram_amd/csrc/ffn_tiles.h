@@ -15,6 +15,13 @@ __device__ __forceinline__ float* z_block(float* z, int row, int col, int I, int
 
 __device__ __forceinline__ float row_gate(const float* gate, int row) { return gate ? 1.f / (1.f + expf(-gate[row])) : 1.f; }
 
+// s (1 - s) from the logit: with s as it is rounded, 1 - s loses its digits where
+// s is near one (0.5 % at a logit of 12, everything from 17.4 on).
+__device__ __forceinline__ float gate_slope(float logit) {
+  const float t = expf(-fabsf(logit)), u = 1.f + t;
+  return t / (u * u);
+}
+
 // A workgroup's tile, its wave's place in it and the results.
 #define FFN_PROLOGUE(C)                                                              \
   __shared__ __align__(1024) char lds[C::LDS];                             \
