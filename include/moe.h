@@ -441,8 +441,9 @@ moe_status_t moe_residual_bwd(const moe_norm_desc_t* desc, const void* x_new,
  * reach 1.21, 2.81 and 3.45), else MOE_ERR_UNSUPPORTED.  A NaN or infinity
  * makes its matrix's X NaN; a zero matrix stays zero, with an eps of 0 too.
  * M and N multiples of 8, at most 2^20, E at most 65535, at most 2^23 tiles of
- * 256 x 256 in all the matrices, 1 to 64 steps, else MOE_ERR_UNSUPPORTED (negative E, M or N, M or N of 0, eps or dtypes that do
- * not exist: MOE_ERR_INVALID_ARG).  E = 0 does nothing. */
+ * 256 x 256 (128 x 128 where a side is below 64) in all the matrices, 1 to 64
+ * steps, else MOE_ERR_UNSUPPORTED (negative E, M or N, M or N of 0, eps or dtypes
+ * that do not exist: MOE_ERR_INVALID_ARG).  E = 0 does nothing. */
 typedef struct {
   int64_t E, M, N;
   int32_t dtype;     /* of G: moe_dtype_t */

@@ -16,8 +16,8 @@ namespace {
 
 constexpr int64_t kMaxSide = int64_t(1) << 20;   // 32-bit offsets within a tile's rows
 
-// Tiles of the largest kind, 256 x 256.
-inline int64_t tiles(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256); }
+// Tiles of the largest kind that a product of m x n results may run on, 256 x 256 unless told.
+inline int64_t tiles(int64_t m, int64_t n, int64_t side = 256) { return ((m + side - 1) / side) * ((n + side - 1) / side); }
 
 inline size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -162,7 +162,7 @@ moe_status_t ortho_check(const moe_ortho_desc_t* d, OrthoLayout* L) {
     return MOE_ERR_INVALID_ARG;
   if (d->M % 8 != 0 || d->N % 8 != 0 || d->M > kMaxSide || d->N > kMaxSide || d->E > 65535 || d->steps < 1 || d->steps > 64)
     return MOE_ERR_UNSUPPORTED;
-  if (d->E * tiles(d->M, d->N) > MAX_TILES) return MOE_ERR_UNSUPPORTED;
+  if (d->E * tiles(d->M, d->N, d->M < ORTHO_NARROW || d->N < ORTHO_NARROW ? 128 : 256) > MAX_TILES) return MOE_ERR_UNSUPPORTED;
   if (!coefficients_ok(d)) return MOE_ERR_UNSUPPORTED;
   const size_t S = (size_t)(d->M < d->N ? d->M : d->N), E = (size_t)d->E;
   L->part = 0;

@@ -66,8 +66,8 @@ inline float tile_time(const TileKind& k, long tiles, long K) {
 }
 
 // The kind of tile that an M x N product over K, `batch` times, is done with
-// soonest, of those from `first` on whose tiles a launch holds (the host checks
-// the largest kind).
+// soonest, of those from `first` on whose tiles a launch holds (the entry points
+// refuse calls whose tiles of the first kind are too many).
 inline int tile_kind(long M, long N, long K, long batch = 1, int first = 0) {
   int best = first;
   float least = 0.f;
