@@ -685,6 +685,7 @@ def ffn_fwd(x, w_gate_up, w_down, gate=None, add=None, act="swiglu", layout="con
             ws=None, out=None, saved=None):
     """Gated feed-forward block of every token (a shared expert, a dense layer):
     add + sigmoid(gate) Wd phi(Wgu x) for x [T,H], w_gate_up [2I,H], w_down [H,I], gate fp32 [T], add [T,H].
+    save: keep the gate and up values for ffn_bwd, in `saved` if given (which is refused without save).
     Returns (out, saved-or-None, ws); `out` may be `add`."""
     return (_native or _block()).ffn_fwd(x, w_gate_up, w_down, gate, *_codes(act, layout), limit, alpha, add, save, ws, out,
                                          saved)

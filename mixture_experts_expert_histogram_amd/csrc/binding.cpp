@@ -292,14 +292,15 @@ const float* gate_of(PyObject* o) { return o == Py_None ? nullptr : (const float
 // ffn_fwd(x, w_gate_up, w_down, gate, act, layout, limit, alpha, add, save, ws, out, saved) -> (out, saved, ws)
 PyObject* ffn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 13, [&] {
+    const int save = PyObject_IsTrue(a[9]);
+    if (save < 0) throw PythonError{};
+    if (!save && a[12] != Py_None) refuse("saved is where save=True puts the gate and up values, without it nothing is saved");
     const Ffn f = ffn(a, a + 4, -1);
     const Tensor &x = THPVariable_Unpack(a[0]), &gu = THPVariable_Unpack(a[1]), &dn = THPVariable_Unpack(a[2]);
     const auto dev = x.device();
     const void* add = input(a[8], "add", x.sizes(), x.scalar_type(), dev);
     const Tensor ws = workspace(a[10], f.fwd, dev), out = output(a[11], "out", x.sizes(), x.scalar_type(), dev);
     std::optional<Tensor> saved;
-    const int save = PyObject_IsTrue(a[9]);
-    if (save < 0) throw PythonError{};
     if (save) saved = workspace(a[12], f.saved, dev);
     launch(dev, "moe_ffn_fwd", [&](hipStream_t s) {
       return moe_ffn_fwd(&f.d, data(x), data(gu), data(dn), gate_of(a[3]), add, data(out), saved ? data(*saved) : nullptr,
