@@ -719,8 +719,9 @@ def norm_bwd(x, w, d_y, d_add=None, eps=1e-5, ws=None, grads=None):
 
 def residual_fwd(x, h, w_post=None, gate=None, scale=1.0, w_next=None, eps=1e-5, x_new=None, y=None):
     """The step after a block: x_new = x + scale gate n with n = w_post h / rms(h) (h without w_post), and the next
-    block's norm y = w_next x_new / rms(x_new) (None without w_next).  x, h [T,H]; w_post, w_next [H]; gate [T,1], [H]
-    or [T,H]; all of one type.  Returns (x_new, y); x_new may be x."""
+    block's norm y = w_next x_new / rms(x_new) (None without w_next).  x, h [T,H]; w_post, w_next [H]; gate [T,1] (one
+    for each token), [H] (one for each channel) or [T,H]; all of one type.  A gate of one dimension is always the
+    channels', also where T = H: ffn_fwd's logits [T] go in as [T,1].  Returns (x_new, y); x_new may be x."""
     return (_native or _block()).residual_fwd(x, h, w_post, gate, scale, w_next, eps, x_new, y)
 
 
