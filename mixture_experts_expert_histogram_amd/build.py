@@ -45,39 +45,55 @@ def binding_commands(obj: str, out: str):
              "-Wl,-rpath," + os.path.join(t, "lib"), LIB_PATH, "-Wl,-rpath,$ORIGIN"])
 
 
-def build(verbose: bool = False) -> str:
-    """Always recompiles every source and relinks the shared library."""
-    os.makedirs(BUILD, exist_ok=True)
-    cc = hipcc()
+def run_all(what: str, jobs, verbose: bool = False) -> None:
+    """Run the commands of jobs [(name, command)] side by side; RuntimeError names those that fail."""
     procs = []
-    objs = []
-    for src in SOURCES:
-        obj = os.path.join(BUILD, src + ".o")
-        objs.append(obj)
-        cmd = [cc] + compile_flags() + ["-c", os.path.join(CSRC, src), "-o", obj]
+    for name, cmd in jobs:
         if verbose:
             print(" ".join(cmd), flush=True)
-        procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    binding = os.path.join(PKG, BINDING_NAME)
-    compile_binding, link_binding = binding_commands(os.path.join(BUILD, BINDING + ".o"), binding + ".tmp")
-    procs.append((BINDING, subprocess.Popen(compile_binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+        procs.append((name, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
-    for src, p in procs:
+    for name, p in procs:
         out = p.communicate()[0].decode(errors="replace")
         # hipcc's host pass does not know the packed-fp32 feature flag; that warning is harmless
         lines = [l for l in out.splitlines() if "packed-fp32-ops" not in l]
         if lines and (verbose or p.returncode):
             print("\n".join(lines), file=sys.stderr)
         if p.returncode:
-            failed.append(src)
+            failed.append(name)
     if failed:
-        raise RuntimeError("HIP compilation failed: " + ", ".join(failed))
+        raise RuntimeError(what + " failed: " + ", ".join(failed))
+
+
+def build_library(verbose: bool = False) -> str:
+    """The C library: needs hipcc only."""
+    cc = hipcc()
+    objs = [os.path.join(BUILD, src + ".o") for src in SOURCES]
+    run_all("HIP compilation", [(src, [cc] + compile_flags() + ["-c", os.path.join(CSRC, src), "-o", obj])
+                                for src, obj in zip(SOURCES, objs)], verbose)
     tmp = LIB_PATH + ".tmp"
-    cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname," + LIB_NAME, "-o", tmp] + objs
-    subprocess.check_call(cmd)
+    run_all("linking the library", [(LIB_NAME, [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Wl,-soname," + LIB_NAME,
+                                                "-o", tmp] + objs)], verbose)
     os.replace(tmp, LIB_PATH)
-    subprocess.check_call(link_binding)
-    os.replace(binding + ".tmp", binding)
+    return LIB_PATH
+
+
+def build_binding(verbose: bool = False) -> str:
+    """The native half of the Python binding, against the library: needs g++, torch and Python's headers."""
+    out = os.path.join(PKG, BINDING_NAME)
+    compile_binding, link_binding = binding_commands(os.path.join(BUILD, BINDING + ".o"), out + ".tmp")
+    run_all("compiling the Python binding (g++)", [(BINDING, compile_binding)], verbose)
+    run_all("linking the Python binding (g++)", [(BINDING_NAME, link_binding)], verbose)
+    os.replace(out + ".tmp", out)
+    return out
+
+
+def build(verbose: bool = False) -> str:
+    """Always recompiles every source and relinks: the library, then the binding, so that the library is there whole
+    where the binding cannot be built."""
+    os.makedirs(BUILD, exist_ok=True)
+    build_library(verbose)
+    build_binding(verbose)
     return LIB_PATH
 
 
