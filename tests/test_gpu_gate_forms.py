@@ -15,7 +15,8 @@ def test_square_inputs():
     for form, full in ((gate, gate[None, :]), (gate[:, None], gate[:, None])):
         new, _ = moe.residual_fwd(x, h, gate=form)
         want, _ = moe.residual_fwd(x, h, gate=full.expand(n, n).contiguous())
-        assert torch.equal(new, want)
+        # x + gate h in one fused rounding, or with the product rounded first: half a step of either more
+        assert ((new - want).abs() <= 2.0 ** -24 * ((form * h).abs() + new.abs() + want.abs())).all()
         d = moe.residual_bwd(new, h, dx, gate=form).d_gate
         assert d.shape == form.shape
         terms = dx.double() * h.double()
