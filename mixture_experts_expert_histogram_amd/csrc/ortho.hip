@@ -140,9 +140,9 @@ __global__ __launch_bounds__(256) void ortho_scale_kernel(OrthoArgs p, int parts
   __shared__ double red[4];
   const size_t n = (size_t)p.M * p.N, at = n * blockIdx.y;
   const double sum = sum_256((int)threadIdx.x < parts ? p.part[blockIdx.y * ORTHO_PARTS + threadIdx.x] : 0.0, red);
-  // in two factors, whose product may be past fp32's range (eps of 0 and subnormal updates)
-  const double whole = ORTHO_X / (sqrt(sum) + (double)p.eps), part = fmin(whole, 0x1p100);
-  const float f = sum == 0.0 ? 0.f : (float)part, f2 = sum == 0.0 ? 0.f : (float)(whole / part);
+  // in two factors, whose product may be past fp32's range (eps of 0 and subnormal updates; huge ones, an infinite eps)
+  const double whole = ORTHO_X / (sqrt(sum) + (double)p.eps), part = fmin(fmax(whole, 0x1p-100), 0x1p100);
+  const float f = (float)part, f2 = sum == 0.0 ? 0.f : (float)(whole / part + 0.0 * sum);   // NaN with an infinity or NaN in u
   for (size_t i = (blockIdx.x * 256ul + threadIdx.x) * 8; i < n; i += gridDim.x * 2048ul) {
     float u[8];
     load8<F32>(p.g, at + i, u);
