@@ -38,10 +38,11 @@
 // range.  Sums and the polynomial's terms are fp32, the norm is summed in 64 bits
 // (no overflow or underflow of fp32 gradients' squares).
 //
-// 16 matrices of 2880 x 2880, five steps: 8.85 ms, a step 415 us for P, 457 for Q
-// and 872 for X (712 without the pair, whose reads and writes at the tiles' ends
-// have no matrix work beside them), before them 53 us for the norm and 130 for the
-// first X.  The sides are 11.25 tiles of 256, which count as 12, and diagonal tiles
+// 16 matrices of 2880 x 2880, five steps: 8.85 ms, a step 419 us for P (65 % of the
+// matrix cores busy at 1.65 GHz), 460 for Q (57 %) and 888 for X (53 %; 712 and 75
+// % without the pair, whose reads and writes at the tiles' ends have no matrix work
+// beside them), before them 51 us for the norm and 127 for the first X (5.2 and 6.3
+// TB/s).  The sides are 11.25 tiles of 256, which count as 12, and diagonal tiles
 // are whole: P and Q compute 23 % more than half a square, X 14 % more than it
 // needs.
 #include "dense_tiles.h"
@@ -105,7 +106,7 @@ __device__ __forceinline__ double sum_256(double v, double (&red)[4]) {
 
 // The update's squares, summed by workgroup, and a step's new momentum: one
 // pass over g (and m), bound by HBM (a step of 8 matrices of 5760 x 2880 with
-// fp32 gradients: 289 us, 5.5 TB/s).
+// fp32 gradients: 288 us, 5.5 TB/s).
 template <bool F32>
 __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs p) {
   __shared__ double red[4];
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(256) void ortho_norm_kernel(OrthoArgs p) {
 }
 
 // X = u / (|u| + eps), times ORTHO_X, in two halves; a step's u again from g and m'
-// (the same step: 260 us, 5.1 TB/s).
+// (the same step: 300 us, 5.3 TB/s).
 template <bool F32>
 __global__ __launch_bounds__(256) void ortho_scale_kernel(OrthoArgs p, int parts) {
   static_assert(ORTHO_PARTS <= 256, "a partial sum a thread");
