@@ -432,10 +432,11 @@ moe_status_t moe_residual_bwd(const moe_norm_desc_t* desc, const void* x_new,
  *   w_out = (1 - decay) w - lr X(U)
  * m_out may be m and w_out may be w.
  * Iterates are held in 22 bits, of which the products take 11 (fp16), with
- * fp32 sums: after five steps of the usual coefficients X is within 2e-3 of the
+ * fp32 sums: after five steps of the usual coefficients X is about 1e-3 from the
  * exact iteration in the 2-norm, whatever the update's rank, before it is
- * rounded to its type (1e-3 mostly; up to 4e-3 where a side is below 64); the
- * norm is summed in 64 bits.  Coefficients must keep the iterates' singular values,
+ * rounded to its type (up to 4e-3 where a few roundings are all of it: a side
+ * below 64, an update with elements in a few rows or columns only); the norm is
+ * summed in 64 bits.  Coefficients must keep the iterates' singular values,
  * which start at most 1, at most 3 and b x + c x^2 and a + b x + c x^2 at most
  * 14.6 in size over their squares (checked; the usual 3.4445, -4.775, 2.0315
  * reach 1.21, 2.81 and 3.45), else MOE_ERR_UNSUPPORTED.  A NaN or infinity

@@ -30,9 +30,9 @@
 // and diag(Q) in the last two steps.  D is kept in fp32 and takes up what the
 // rounding of the rest of Q's diagonal leaves out; what P's diagonal's rounding
 // takes away goes into Q's.  From the iteration in 64 bits, in the 2-norm: 1.5e-3
-// at most from 64 x 64 on, at any rank, 5e-4 to 8e-4 mostly; up to 4e-3 in matrices
-// of 8 rows, where a few roundings are all of it; a bf16 result's own rounding,
-// 1.66e-3, comes on top.  (With all of Q's products on the pair: 1e-4 to 1.1e-3,
+// at most from 64 x 64 on, at any rank, 5e-4 to 8e-4 mostly; up to 4e-3 where a few
+// roundings are all of it (8 rows, or elements in a few rows or columns only); a
+// bf16 result's own rounding, 1.66e-3, comes on top.  (With all of Q's products on the pair: 1e-4 to 1.1e-3,
 // for another 2 S^2 L operations a step.)
 // Factors 2^6 on X and 2^12 on P and Q keep small elements out of the subnormal
 // range.  Sums and the polynomial's terms are fp32, the norm is summed in 64 bits
